@@ -1,4 +1,4 @@
-"""ctypes binding of libmoecache.so (include/moe_cache.h).
+"""ctypes binding of libmoecache.so (include/moe_cache.h, include/moe_attn.h).
 
 Argument marshalling only: every step of the hot path runs in the library's
 CUDA kernels.  Device buffers may be passed as torch tensors (their
@@ -80,12 +80,36 @@ class moe_cache_timing(C.Structure):
                 ("up_n", C.c_uint64), ("down_n", C.c_uint64)]
 
 
+class moe_norm_args(C.Structure):
+    _fields_ = ([("dtype", C.c_int), ("hidden", C.c_int), ("tokens", C.c_longlong)]
+                + [(n, C.c_void_p) for n in ("x_d", "block_d", "post_w_d", "gate_d", "pre_w_d", "x_out_d", "y_d")]
+                + [(n, C.c_longlong) for n in ("x_row", "block_row", "gate_row", "x_out_row", "y_row")]
+                + [("gate_col", C.c_int), ("res_scale", C.c_float), ("eps", C.c_float)])
+
+
+class moe_kv_pages(C.Structure):
+    _fields_ = ([(n, C.c_int) for n in ("dtype", "layers", "kv_heads", "head_dim", "page_tokens", "num_pages",
+                                        "max_seqs", "max_pages")]
+                + [(n, C.c_void_p) for n in ("k_d", "v_d", "table_d", "lens_d", "refs_d", "status_d", "work_d")]
+                + [("work_bytes", C.c_size_t)])
+
+
+class moe_prompt_args(C.Structure):
+    _fields_ = ([(n, C.c_int) for n in ("dtype", "heads", "kv_heads", "head_dim", "n", "q_tokens", "k_tokens")]
+                + [(n, C.c_void_p) for n in ("starts_q_d", "starts_k_d", "q_d", "k_d", "v_d", "out_d", "lse_d")]
+                + [(n, C.c_longlong) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+                                               "out_token", "out_head")]
+                + [("scale", C.c_float), ("window", C.c_int)])
+
+
 _H = C.c_void_p
 _P = C.c_void_p
 _I = C.c_int
+_L = C.c_longlong
 _S = C.c_int
+_KV = C.POINTER(moe_kv_pages)
 
-# name -> (restype, argtypes); every symbol include/moe_cache.h declares
+# name -> (restype, argtypes); every symbol include/*.h declares
 SIGNATURES = {
     "moe_cache_create": (_S, [C.POINTER(moe_cache_config), C.POINTER(_H)]),
     "moe_cache_destroy": (None, [_H]),
@@ -112,6 +136,17 @@ SIGNATURES = {
     "moe_cache_read_timing": (_S, [_H, C.POINTER(moe_cache_timing)]),
     "moe_cache_read_timing_launches": (_S, [_H, _P, _P, _I, C.POINTER(_I)]),
     "moe_cache_read_copy_spans": (_S, [_H, _P, _I, C.POINTER(_I)]),
+    "moe_norm_residual": (_S, [C.POINTER(moe_norm_args), _P]),
+    "moe_kv_work_bytes": (_S, [_KV, _I, C.POINTER(C.c_size_t)]),
+    "moe_kv_reserve": (_S, [_KV, _P, _P, _I, _P]),
+    "moe_kv_append": (_S, [_KV, _I, _P, _P, _I, _P, _L, _L, _P, _L, _L, _I, _P]),
+    "moe_kv_truncate": (_S, [_KV, _P, _P, _I, _P]),
+    "moe_kv_fork": (_S, [_KV, _P, _P, _I, _P]),
+    "moe_kv_copy": (_S, [_KV, _P, _P, _I, _P]),
+    "moe_kv_compact": (_S, [_KV, _P, _P, _P, _P]),
+    "moe_kv_check": (_S, [_KV, _P]),
+    "moe_attn_decode": (_S, [_KV, _I, _P, _L, _L, _P, _I, _I, C.c_float, _I, _P, _L, _L, _P, _P]),
+    "moe_attn_prompt": (_S, [C.POINTER(moe_prompt_args), _P]),
 }
 
 _lib = None

@@ -1,0 +1,209 @@
+// C entry points of moe_attn.h: argument checks, then the launchers.
+#include <cuda_runtime.h>
+
+#include "attn_common.cuh"
+
+using namespace moe;
+
+namespace {
+
+moe_status done(cudaError_t e) {
+  return e == cudaSuccess ? MOE_OK : set_global_error(MOE_ECUDA, cudaGetErrorString(e));
+}
+
+bool hidden_type(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+
+// addresses of elements of the type start on its size
+bool on_element(int dtype, const void* p) { return ((size_t)p & (dtype == MOE_BF16 ? 1 : 3)) == 0; }
+
+// null if the cache's description is usable
+const char* kv_sizes(const moe_kv_pages* kv) {
+  if (!kv) return "null cache";
+  if (!hidden_type(kv->dtype)) return "dtype must be MOE_F32 or MOE_BF16";
+  if (kv->layers < 1 || kv->kv_heads < 1 || kv->kv_heads > 4096) return "bad layers or kv_heads";
+  if (kv->head_dim < 8 || kv->head_dim > MOE_ATTN_MAX_HEAD_DIM || kv->head_dim % 8)
+    return "head_dim must be a multiple of 8 up to MOE_ATTN_MAX_HEAD_DIM";
+  if (kv->page_tokens < 1 || kv->page_tokens > 1024 || (kv->page_tokens & (kv->page_tokens - 1)))
+    return "page_tokens must be a power of two up to 1024";
+  if (kv->num_pages < 1 || kv->num_pages > (1 << 28)) return "bad num_pages";
+  if (kv->max_seqs < 1 || kv->max_seqs > MOE_KV_MAX_SEQS) return "max_seqs must be in 1..MOE_KV_MAX_SEQS";
+  if (kv->max_pages < 1 || kv->max_pages > (1 << 20) || (long long)kv->max_pages * kv->page_tokens > 0x40000000ll)
+    return "bad max_pages";
+  return nullptr;
+}
+
+const char* kv_bad(const moe_kv_pages* kv) {
+  if (const char* why = kv_sizes(kv)) return why;
+  if (!kv->k_d || !kv->v_d || !kv->table_d || !kv->lens_d || !kv->refs_d || !kv->status_d || !kv->work_d)
+    return "null buffer in the cache";
+  if (!attn::aligned(16, kv->k_d, kv->v_d)) return "K and V pools must be 16-byte aligned";
+  if (!attn::aligned(4, kv->table_d, kv->lens_d, kv->refs_d, kv->status_d)) return "misaligned bookkeeping array";
+  if (!attn::aligned(256, kv->work_d)) return "work_d must be 256-byte aligned";
+  if (kv->work_bytes < kv_work_bytes(*kv)) return "work_bytes is smaller than moe_kv_work_bytes";
+  return nullptr;
+}
+
+moe_status fail(const char* why) { return set_global_error(MOE_EINVAL, why); }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_norm_residual(const moe_norm_args* a, moe_stream_t stream) {
+  if (!a || !hidden_type(a->dtype)) return fail("moe_norm_residual: dtype must be MOE_F32 or MOE_BF16");
+  if (a->hidden < 1 || a->hidden > MOE_NORM_MAX_HIDDEN) return fail("moe_norm_residual: hidden out of range");
+  if (a->tokens < 0) return fail("moe_norm_residual: negative tokens");
+  if (!(a->eps >= 0.f)) return fail("moe_norm_residual: eps must not be negative");
+  if (a->gate_col != 0 && a->gate_col != 1) return fail("moe_norm_residual: gate_col must be 0 or 1");
+  if (a->tokens == 0) return MOE_OK;
+  if (!a->x_d) return fail("moe_norm_residual: null x");
+  if (!a->block_d && (a->post_w_d || a->gate_d)) return fail("moe_norm_residual: post_w or gate without a block");
+  if (!a->x_out_d && !a->y_d) return fail("moe_norm_residual: no output");
+  if (a->y_d && !a->pre_w_d) return fail("moe_norm_residual: y without pre_w");
+  if (a->x_out_d && a->x_out_d == a->y_d) return fail("moe_norm_residual: x_out and y are the same buffer");
+  if (a->x_row < 0 || a->block_row < 0 || a->gate_row < 0) return fail("moe_norm_residual: negative row distance");
+  if (a->tokens > 1 && ((a->x_out_d && a->x_out_row < a->hidden) || (a->y_d && a->y_row < a->hidden)))
+    return fail("moe_norm_residual: output rows overlap");
+  const void* out[2] = {a->x_out_d, a->y_d};
+  const long long out_row[2] = {a->x_out_row, a->y_row};
+  for (int i = 0; i < 2; ++i)
+    if (out[i] && a->tokens > 1 &&
+        ((out[i] == a->x_d && out_row[i] != a->x_row) || (out[i] == a->block_d && out_row[i] != a->block_row)))
+      return fail("moe_norm_residual: an output in place of an input needs its row distance");
+  const void* all[] = {a->x_d, a->block_d, a->post_w_d, a->gate_d, a->pre_w_d, a->x_out_d, a->y_d};
+  for (const void* p : all)
+    if (!on_element(a->dtype, p)) return fail("moe_norm_residual: misaligned buffer");
+  return done(launch_norm(*a, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_work_bytes(const moe_kv_pages* kv, int max_heads, size_t* bytes) {
+  if (const char* why = kv_sizes(kv)) return fail(why);
+  if (!bytes || max_heads < 1 || max_heads % kv->kv_heads || max_heads / kv->kv_heads > MOE_ATTN_MAX_GROUP)
+    return fail("moe_kv_work_bytes: bad max_heads or null result");
+  *bytes = kv_work_bytes(*kv) + attn_decode_work_bytes(*kv, max_heads);
+  return MOE_OK;
+}
+
+moe_status moe_kv_reserve(const moe_kv_pages* kv, const int32_t* seqs_d, const int32_t* counts_d, int n,
+                          moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (n < 0 || n > kv->max_seqs) return fail("moe_kv_reserve: n out of range");
+  if (n == 0) return MOE_OK;
+  if (!seqs_d || !counts_d) return fail("moe_kv_reserve: null list");
+  return done(launch_kv_reserve(*kv, seqs_d, counts_d, n, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_append(const moe_kv_pages* kv, int layer, const int32_t* seqs_d, const int32_t* starts_d, int n,
+                         const void* k_new_d, long long k_token, long long k_head, const void* v_new_d,
+                         long long v_token, long long v_head, int tokens, moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (layer < 0 || layer >= kv->layers) return fail("moe_kv_append: layer out of range");
+  if (n < 0 || n > kv->max_seqs || tokens < 0) return fail("moe_kv_append: n or tokens out of range");
+  if (n == 0 || tokens == 0) return MOE_OK;
+  if (!seqs_d || !starts_d || !k_new_d || !v_new_d) return fail("moe_kv_append: null buffer");
+  if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0) return fail("moe_kv_append: negative distance");
+  if (!on_element(kv->dtype, k_new_d) || !on_element(kv->dtype, v_new_d))
+    return fail("moe_kv_append: misaligned buffer");
+  return done(launch_kv_append(*kv, layer, seqs_d, starts_d, n, k_new_d, k_token, k_head, v_new_d, v_token, v_head,
+                               tokens, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_truncate(const moe_kv_pages* kv, const int32_t* seqs_d, const int32_t* new_lens_d, int n,
+                           moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (n < 0 || n > kv->max_seqs) return fail("moe_kv_truncate: n out of range");
+  if (n == 0) return MOE_OK;
+  if (!seqs_d) return fail("moe_kv_truncate: null list");
+  return done(launch_kv_truncate(*kv, seqs_d, new_lens_d, n, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_fork(const moe_kv_pages* kv, const int32_t* src_d, const int32_t* dst_d, int n,
+                       moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (n < 0 || n > kv->max_seqs) return fail("moe_kv_fork: n out of range");
+  if (n == 0) return MOE_OK;
+  if (!src_d || !dst_d) return fail("moe_kv_fork: null list");
+  return done(launch_kv_fork(*kv, src_d, dst_d, n, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_copy(const moe_kv_pages* kv, const int32_t* src_d, const int32_t* dst_d, int n,
+                       moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (n < 0 || n > kv->num_pages) return fail("moe_kv_copy: n out of range");
+  if (n == 0) return MOE_OK;
+  if (!src_d || !dst_d) return fail("moe_kv_copy: null list");
+  return done(launch_kv_copy(*kv, src_d, dst_d, n, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_compact(const moe_kv_pages* kv, int32_t* table_out_d, int32_t* refs_out_d, int32_t* used_d,
+                          moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (!table_out_d || !refs_out_d) return fail("moe_kv_compact: null output");
+  return done(launch_kv_compact(*kv, table_out_d, refs_out_d, used_d, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_check(const moe_kv_pages* kv, moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  int32_t code = 0;
+  cudaError_t e = cudaMemcpyAsync(&code, kv->status_d, sizeof(code), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return done(e);
+  switch (code) {
+    case MOE_KV_OK: return MOE_OK;
+    case MOE_KV_BAD_SEQ: return set_global_error(MOE_ESTATE, "a sequence out of range, or twice in a list");
+    case MOE_KV_BAD_COUNT: return set_global_error(MOE_ESTATE, "a negative count or length");
+    case MOE_KV_TOO_LONG: return set_global_error(MOE_ESTATE, "a sequence longer than max_pages pages");
+    case MOE_KV_NO_PAGES: return set_global_error(MOE_ESTATE, "too few free pages");
+    case MOE_KV_BAD_PAGE: return set_global_error(MOE_ESTATE, "no valid page where a token should be");
+  }
+  return set_global_error(MOE_ESTATE, "unknown status");
+}
+
+moe_status moe_attn_decode(const moe_kv_pages* kv, int layer, const void* q_d, long long q_token, long long q_head,
+                           const int32_t* seqs_d, int n, int heads, float scale, int window, void* out_d,
+                           long long out_token, long long out_head, float* lse_d, moe_stream_t stream) {
+  if (const char* why = kv_bad(kv)) return fail(why);
+  if (layer < 0 || layer >= kv->layers) return fail("moe_attn_decode: layer out of range");
+  if (heads < 1 || heads % kv->kv_heads || heads / kv->kv_heads > MOE_ATTN_MAX_GROUP)
+    return fail("moe_attn_decode: heads must be 1..MOE_ATTN_MAX_GROUP times kv_heads");
+  if (n < 0 || n > MOE_KV_MAX_SEQS - 1) return fail("moe_attn_decode: n out of range");
+  if (window < 0) return fail("moe_attn_decode: negative window");
+  if (!(scale - scale == 0.f)) return fail("moe_attn_decode: scale is not finite");
+  if (n == 0) return MOE_OK;
+  if (!q_d || !seqs_d || !out_d) return fail("moe_attn_decode: null buffer");
+  if (q_token < 0 || q_head < 0 || (heads > 1 && out_head < kv->head_dim) || (n > 1 && out_token < kv->head_dim))
+    return fail("moe_attn_decode: bad distance");
+  if (!on_element(kv->dtype, q_d) || !on_element(kv->dtype, out_d)) return fail("moe_attn_decode: misaligned buffer");
+  if (kv->work_bytes < kv_work_bytes(*kv) + attn_decode_work_bytes(*kv, heads))
+    return fail("moe_attn_decode: work_bytes is smaller than moe_kv_work_bytes for these heads");
+  const DecodeArgs a = {q_d, q_token, q_head, seqs_d, n, heads, layer, scale, window, out_d, out_token, out_head, lse_d};
+  return done(launch_attn_decode(*kv, a, (cudaStream_t)stream));
+}
+
+moe_status moe_attn_prompt(const moe_prompt_args* a, moe_stream_t stream) {
+  if (!a || !hidden_type(a->dtype)) return fail("moe_attn_prompt: dtype must be MOE_F32 or MOE_BF16");
+  if (a->head_dim < 8 || a->head_dim > MOE_ATTN_MAX_HEAD_DIM || a->head_dim % 8)
+    return fail("moe_attn_prompt: head_dim must be a multiple of 8 up to MOE_ATTN_MAX_HEAD_DIM");
+  if (a->kv_heads < 1 || a->heads < 1 || a->heads % a->kv_heads || a->heads / a->kv_heads > MOE_ATTN_MAX_GROUP ||
+      a->heads > 65535)
+    return fail("moe_attn_prompt: heads must be 1..MOE_ATTN_MAX_GROUP times kv_heads");
+  if (a->n < 0 || a->n > MOE_KV_MAX_SEQS || a->q_tokens < 0 || a->k_tokens < 0 || a->q_tokens > 0x40000000 ||
+      a->k_tokens > 0x40000000)
+    return fail("moe_attn_prompt: n or tokens out of range");
+  if (a->window < 0) return fail("moe_attn_prompt: negative window");
+  if (!(a->scale - a->scale == 0.f)) return fail("moe_attn_prompt: scale is not finite");
+  if (a->n == 0 || a->q_tokens == 0) return MOE_OK;
+  if (!a->q_d || !a->out_d || !a->starts_q_d || !a->starts_k_d || (a->k_tokens > 0 && (!a->k_d || !a->v_d)))
+    return fail("moe_attn_prompt: null buffer");
+  const long long d[] = {a->q_token, a->q_head, a->k_token, a->k_head, a->v_token, a->v_head};
+  for (long long x : d)
+    if (x < 0) return fail("moe_attn_prompt: negative distance");
+  if ((a->heads > 1 && a->out_head < a->head_dim) || (a->q_tokens > 1 && a->out_token < a->head_dim))
+    return fail("moe_attn_prompt: output rows overlap");
+  if (!on_element(a->dtype, a->q_d) || !on_element(a->dtype, a->k_d) || !on_element(a->dtype, a->v_d) ||
+      !on_element(a->dtype, a->out_d))
+    return fail("moe_attn_prompt: misaligned buffer");
+  return done(launch_attn_prompt(*a, (cudaStream_t)stream));
+}
+
+}  // extern "C"

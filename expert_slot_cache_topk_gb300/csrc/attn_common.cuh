@@ -1,0 +1,123 @@
+// Shared by the kernels of the attention half of a decoder layer (k_norm.cu,
+// k_kv_pages.cu, k_attn_decode.cu, k_attn_prompt*.cu): loads and stores of f32
+// and bf16 vectors as f32, block sums, and the launchers' declarations.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "internal.cuh"
+#include "moe_attn.h"
+
+namespace moe {
+namespace attn {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// N consecutive elements as f32; N * sizeof(T) is 16 or 32 (16-byte aligned), or N is 1
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* __restrict__ p, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = Elem<T>::get(p);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p + i);
+      v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p + i);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[i + 2 * j] = __uint_as_float(w[j] << 16);
+        v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    Elem<T>::put(p, v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                                                    pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+  }
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// true if every one of the addresses and byte distances is a multiple of `to`
+template <typename... A>
+inline bool aligned(size_t to, A... a) {
+  return ((((size_t)a) % to == 0) && ...);
+}
+
+}  // namespace attn
+
+cudaError_t launch_norm(const moe_norm_args& a, cudaStream_t s);
+cudaError_t launch_kv_reserve(const moe_kv_pages& kv, const int32_t* seqs, const int32_t* counts, int n, cudaStream_t s);
+cudaError_t launch_kv_append(const moe_kv_pages& kv, int layer, const int32_t* seqs, const int32_t* starts, int n,
+                             const void* k, long long k_token, long long k_head, const void* v, long long v_token,
+                             long long v_head, int tokens, cudaStream_t s);
+cudaError_t launch_kv_truncate(const moe_kv_pages& kv, const int32_t* seqs, const int32_t* lens, int n, cudaStream_t s);
+cudaError_t launch_kv_fork(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
+cudaError_t launch_kv_copy(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
+cudaError_t launch_kv_compact(const moe_kv_pages& kv, int32_t* table_out, int32_t* refs_out, int32_t* used,
+                              cudaStream_t s);
+
+// One launch of decode attention (moe_attn_decode's arguments, checked)
+struct DecodeArgs {
+  const void* q;
+  long long q_token, q_head;
+  const int32_t* seqs;
+  int n, heads, layer;
+  float scale;
+  int window;
+  void* out;
+  long long out_token, out_head;
+  float* lse;
+};
+cudaError_t launch_attn_decode(const moe_kv_pages& kv, const DecodeArgs& a, cudaStream_t s);
+size_t attn_decode_work_bytes(const moe_kv_pages& kv, int max_heads);
+size_t kv_work_bytes(const moe_kv_pages& kv);   // bytes the page calls use at the start of work_d
+
+cudaError_t launch_attn_prompt(const moe_prompt_args& a, cudaStream_t s);
+
+}  // namespace moe

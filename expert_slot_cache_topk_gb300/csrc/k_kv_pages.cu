@@ -1,0 +1,540 @@
+// The pages of a key-value cache: reserve, append, truncate, fork, copy and
+// compact.  All bookkeeping is on the device (no read-back), deterministic
+// (pages are handed out lowest free index first) and all or nothing: a call
+// whose lists are wrong sets the status word and changes nothing.
+//
+// What bounds these calls: the bookkeeping is a few kilobytes and costs
+// launches and dependent loads; append, the private copies of shared pages and
+// compaction move K and V bytes once (read + write).
+#include "attn_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace attn;
+
+constexpr int kBookThreads = 1024;
+constexpr int kBookWarps = kBookThreads / 32;
+
+struct Kv {
+  char *k, *v;
+  int32_t *table, *lens, *refs, *status;
+  int num_pages, max_seqs, max_pages, page_shift, layers, kv_heads;
+  long long token_bytes;     // one head's row: head_dim * element size
+  // workspace
+  int32_t* hdr;              // [64]: [0] copies, [1] error of the running call, [2] movers
+  int32_t* mark;             // [max_seqs]
+  int32_t* off;              // [max_seqs + 1]
+  int32_t* list_a;           // [num_pages]
+  int32_t* list_b;           // [num_pages]
+  int32_t* cp;               // [3 * max_seqs]: private copies (from, to, tokens)
+  int32_t* rows;             // [max_seqs * max_pages]
+};
+
+enum { H_COPIES = 0, H_ERR = 1, H_MOVES = 2 };
+constexpr size_t kHdrInts = 64;
+
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+Kv make(const moe_kv_pages& m) {
+  Kv d;
+  d.k = (char*)m.k_d, d.v = (char*)m.v_d;
+  d.table = m.table_d, d.lens = m.lens_d, d.refs = m.refs_d, d.status = m.status_d;
+  d.num_pages = m.num_pages, d.max_seqs = m.max_seqs, d.max_pages = m.max_pages;
+  d.page_shift = log2_of(m.page_tokens);
+  d.layers = m.layers, d.kv_heads = m.kv_heads;
+  d.token_bytes = (long long)m.head_dim * (m.dtype == MOE_BF16 ? 2 : 4);
+  int32_t* w = (int32_t*)m.work_d;
+  d.hdr = w, w += kHdrInts;
+  d.mark = w, w += m.max_seqs;
+  d.off = w, w += m.max_seqs + 1;
+  d.list_a = w, w += m.num_pages;
+  d.list_b = w, w += m.num_pages;
+  d.cp = w, w += 3 * (size_t)m.max_seqs;
+  d.rows = w;
+  return d;
+}
+
+__device__ __forceinline__ void set_status(int32_t* status, int code) { atomicCAS(status, MOE_KV_OK, code); }
+
+__device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
+
+// Exclusive sum over the block of one int per thread; *total = the block's sum
+__device__ __forceinline__ int block_scan(int v, int* total) {
+  __shared__ int part[kBookWarps + 1];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kAll, s, o);
+    if (lane >= o) s += u;
+  }
+  __syncthreads();                       // part of the previous call is read
+  if (lane == 31) part[w] = s;
+  __syncthreads();
+  if (w == 0) {
+    const int x = lane < kBookWarps ? part[lane] : 0;
+    int y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kAll, y, o);
+      if (lane >= o) y += u;
+    }
+    part[lane] = y - x;
+    if (lane == 31) part[kBookWarps] = y;
+  }
+  __syncthreads();
+  *total = part[kBookWarps];
+  return part[w] + s - v;
+}
+
+// One block: n rows, in list order.
+__global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int32_t* __restrict__ seqs,
+                                                          const int32_t* __restrict__ counts, int n) {
+  __shared__ int bad, ncopy;
+  const int t = threadIdx.x;
+  if (t == 0) bad = 0, ncopy = 0, d.hdr[H_COPIES] = 0;
+  __syncthreads();
+  for (int i = t; i < n; i += kBookThreads) {
+    const int s = seqs[i];
+    if ((unsigned)s >= (unsigned)d.max_seqs) bad = MOE_KV_BAD_SEQ;
+    else d.mark[s] = i;
+  }
+  __syncthreads();
+  if (bad) {
+    if (t == 0) set_status(d.status, bad);
+    return;
+  }
+  // pages wanted by each row, and where its run of them starts
+  int base = 0;
+  for (int i0 = 0; i0 < n; i0 += kBookThreads) {
+    const int i = i0 + t;
+    int want = 0;
+    if (i < n) {
+      const int s = seqs[i], c = counts[i], held = d.lens[s];
+      const long long after = (long long)held + c;
+      if (d.mark[s] != i) bad = MOE_KV_BAD_SEQ;
+      else if (c < 0 || held < 0) bad = MOE_KV_BAD_COUNT;
+      else if (after > ((long long)d.max_pages << d.page_shift) || after > 0x7fffffffll) bad = MOE_KV_TOO_LONG;
+      else {
+        want = pages_of((int)after, d.page_shift) - pages_of(held, d.page_shift);
+        if (c > 0 && (held & ((1 << d.page_shift) - 1))) {
+          const int p = d.table[(size_t)s * d.max_pages + (held >> d.page_shift)];
+          if ((unsigned)p >= (unsigned)d.num_pages) bad = MOE_KV_BAD_PAGE;
+          else if (d.refs[p] > 1) ++want;
+        }
+      }
+    }
+    int total;
+    const int at = block_scan(want, &total);
+    if (i < n) d.off[i] = base + at;
+    base += total;
+    if (base > d.num_pages) break;       // more than there are pages: refused below
+  }
+  if (t == 0) d.off[n] = base;
+  __syncthreads();
+  if (bad || base > d.num_pages) {
+    if (t == 0) set_status(d.status, bad ? bad : MOE_KV_NO_PAGES);
+    return;
+  }
+  // the lowest `base` free pages, ascending
+  int found = 0;
+  for (int p0 = 0; p0 < d.num_pages && found < base; p0 += 4 * kBookThreads) {
+    int free4[4], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int p = p0 + 4 * t + j;
+      free4[j] = p < d.num_pages && d.refs[p] <= 0;
+      mine += free4[j];
+    }
+    int total;
+    int at = found + block_scan(mine, &total);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (free4[j]) {
+        if (at < base) d.list_a[at] = p0 + 4 * t + j;
+        ++at;
+      }
+    found += total;
+  }
+  __syncthreads();
+  if (found < base) {
+    if (t == 0) set_status(d.status, MOE_KV_NO_PAGES);
+    return;
+  }
+  // hand them out: page r of the list goes to the row whose run holds r.  Shared
+  // pages are judged by the counts as they were: the reads come before any change.
+  for (int i = t; i < n; i += kBookThreads) {
+    const int s = seqs[i], held = d.lens[s], after = held + counts[i];
+    const int fresh = pages_of(after, d.page_shift) - pages_of(held, d.page_shift);
+    d.mark[s] = d.off[i + 1] - d.off[i] > fresh;         // 1: the run starts with a private copy
+  }
+  __syncthreads();
+  for (int r = t; r < base; r += kBookThreads) {
+    int lo = 0, hi = n;                                   // off[lo] <= r < off[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (d.off[mid] <= r) lo = mid;
+      else hi = mid;
+    }
+    const int s = seqs[lo], held = d.lens[s], page = d.list_a[r];
+    const int col = pages_of(held, d.page_shift) + (r - d.off[lo]) - d.mark[s];
+    int32_t* cell = d.table + (size_t)s * d.max_pages + col;
+    if (d.mark[s] && r == d.off[lo]) {
+      const int c = atomicAdd(&ncopy, 1);                 // the order of copies does not matter
+      const int old = *cell;
+      d.cp[3 * c] = old, d.cp[3 * c + 1] = page, d.cp[3 * c + 2] = held & ((1 << d.page_shift) - 1);
+      atomicSub(&d.refs[old], 1);
+    }
+    *cell = page;
+    d.refs[page] = 1;
+  }
+  __syncthreads();
+  for (int i = t; i < n; i += kBookThreads) d.lens[seqs[i]] += counts[i];
+  if (t == 0) d.hdr[H_COPIES] = ncopy;
+}
+
+// Whole 16-byte (or, for odd head sizes, narrower) units of `bytes` contiguous bytes
+template <typename U>
+__device__ __forceinline__ void copy_units(const char* __restrict__ src, char* __restrict__ dst, long long bytes, int t,
+                                           int threads) {
+  const U* s = reinterpret_cast<const U*>(src);
+  U* o = reinterpret_cast<U*>(dst);
+  const long long n = bytes / (long long)sizeof(U);
+  long long i = t;
+  for (; i + 3 * threads < n; i += 4 * threads) {
+    const U a = s[i], b = s[i + threads], c = s[i + 2 * threads], e = s[i + 3 * threads];
+    o[i] = a, o[i + threads] = b, o[i + 2 * threads] = c, o[i + 3 * threads] = e;
+  }
+  for (; i < n; i += threads) o[i] = s[i];
+}
+
+// Private copies of shared last pages: the tokens held, every layer, K and V
+__global__ void __launch_bounds__(256) k_copy_tails(const Kv d) {
+  const int copies = d.hdr[H_COPIES];
+  const long long head_bytes = d.token_bytes << d.page_shift;
+  const long long page_bytes = head_bytes * d.kv_heads;
+  const long long items = (long long)copies * d.layers * 2 * d.kv_heads;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int h = (int)(it % d.kv_heads);
+    const int side = (int)(it / d.kv_heads % 2);
+    const int layer = (int)(it / (2 * d.kv_heads) % d.layers);
+    const int c = (int)(it / (2ll * d.kv_heads * d.layers));
+    char* pool = side ? d.v : d.k;
+    const long long at = (long long)layer * d.num_pages * page_bytes + h * head_bytes;
+    copy_units<uint4>(pool + at + d.cp[3 * c] * page_bytes, pool + at + d.cp[3 * c + 1] * page_bytes,
+                      d.cp[3 * c + 2] * d.token_bytes, threadIdx.x, blockDim.x);
+  }
+}
+
+// Whole pages from list_src[i] to list_dst[i], i < n (n on the device when n_d is given)
+__global__ void __launch_bounds__(256) k_copy_pages(const Kv d, const int32_t* __restrict__ src,
+                                                    const int32_t* __restrict__ dst, int n,
+                                                    const int32_t* __restrict__ n_d) {
+  if (n_d) n = *n_d;
+  const long long page_bytes = (d.token_bytes << d.page_shift) * d.kv_heads;
+  const long long part = page_bytes < 65536 ? page_bytes : 65536;   // bytes of one item
+  const int parts = (int)((page_bytes + part - 1) / part);
+  const long long items = (long long)n * d.layers * 2 * parts;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int q = (int)(it % parts);
+    const int side = (int)(it / parts % 2);
+    const int layer = (int)(it / (2 * parts) % d.layers);
+    const int i = (int)(it / (2ll * parts * d.layers));
+    const int from = src[i], to = dst[i];
+    if ((unsigned)from >= (unsigned)d.num_pages || (unsigned)to >= (unsigned)d.num_pages) {
+      if (threadIdx.x == 0) set_status(d.status, MOE_KV_BAD_PAGE);
+      continue;
+    }
+    char* pool = (side ? d.v : d.k) + (long long)layer * d.num_pages * page_bytes + q * part;
+    const long long left = page_bytes - q * part;
+    copy_units<uint4>(pool + from * page_bytes, pool + to * page_bytes, left < part ? left : part, threadIdx.x,
+                      blockDim.x);
+  }
+}
+
+// A list of rows is in range and has no row twice.  Each block decides for
+// itself from the same inputs, so that all of them go on or none does.
+__device__ __forceinline__ int check_rows(const int32_t* __restrict__ rows, int n, int max_seqs, unsigned* bits,
+                                          bool distinct) {
+  __shared__ int bad;
+  if (threadIdx.x == 0) bad = 0;
+  if (distinct)
+    for (int i = threadIdx.x; i < (max_seqs + 31) / 32; i += blockDim.x) bits[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int s = rows[i];
+    if ((unsigned)s >= (unsigned)max_seqs) bad = MOE_KV_BAD_SEQ;
+    else if (distinct && (atomicOr(&bits[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u)) bad = MOE_KV_BAD_SEQ;
+  }
+  __syncthreads();
+  const int r = bad;
+  __syncthreads();
+  return r;
+}
+
+__global__ void __launch_bounds__(256) k_truncate(const Kv d, const int32_t* __restrict__ seqs,
+                                                  const int32_t* __restrict__ lens, int n) {
+  extern __shared__ unsigned bits[];
+  __shared__ int neg;
+  if (threadIdx.x == 0) neg = 0;
+  int bad = check_rows(seqs, n, d.max_seqs, bits, true);
+  if (lens)
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+      if (lens[i] < 0) neg = 1;
+  __syncthreads();
+  if (neg) bad = bad ? bad : MOE_KV_BAD_COUNT;
+  if (bad) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(d.status, bad);
+    return;
+  }
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int s = seqs[i], held = d.lens[s];
+    const int want = lens ? lens[i] : 0;
+    const int keep = want < held ? want : held;
+    int last = pages_of(held, d.page_shift);
+    if (last > d.max_pages) last = d.max_pages;
+    for (int c = pages_of(keep, d.page_shift) + threadIdx.x; c < last; c += blockDim.x) {
+      int32_t* cell = d.table + (size_t)s * d.max_pages + c;
+      const int p = *cell;
+      if ((unsigned)p < (unsigned)d.num_pages) atomicSub(&d.refs[p], 1);
+      *cell = -1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) d.lens[s] = keep;
+  }
+}
+
+// Fork, first launch: the sources' rows as they are, and one more reference each
+__global__ void __launch_bounds__(256) k_fork_read(const Kv d, const int32_t* __restrict__ src,
+                                                   const int32_t* __restrict__ dst, int n) {
+  extern __shared__ unsigned bits[];
+  const int bad = check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true);
+  if (bad) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(d.status, MOE_KV_BAD_SEQ);
+    return;
+  }
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int s = src[i];
+    int cols = pages_of(d.lens[s], d.page_shift);
+    if (cols > d.max_pages) cols = d.max_pages;
+    if (threadIdx.x == 0) d.mark[i] = d.lens[s];
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+      const int p = d.table[(size_t)s * d.max_pages + c];
+      d.rows[(size_t)i * d.max_pages + c] = p;
+      if ((unsigned)p < (unsigned)d.num_pages) atomicAdd(&d.refs[p], 1);
+    }
+  }
+}
+
+// Fork, second launch: release what the destinations held, write their rows
+__global__ void __launch_bounds__(256) k_fork_write(const Kv d, const int32_t* __restrict__ src,
+                                                    const int32_t* __restrict__ dst, int n) {
+  extern __shared__ unsigned bits[];
+  if (check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true)) return;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int s = dst[i], held = d.lens[s], now = d.mark[i];
+    int old = pages_of(held, d.page_shift), cols = pages_of(now, d.page_shift);
+    if (old > d.max_pages) old = d.max_pages;
+    if (cols > d.max_pages) cols = d.max_pages;
+    const int all = old > cols ? old : cols;
+    for (int c = threadIdx.x; c < all; c += blockDim.x) {
+      int32_t* cell = d.table + (size_t)s * d.max_pages + c;
+      if (c < old) {
+        const int p = *cell;
+        if ((unsigned)p < (unsigned)d.num_pages) atomicSub(&d.refs[p], 1);
+      }
+      *cell = c < cols ? d.rows[(size_t)i * d.max_pages + c] : -1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) d.lens[s] = now;
+  }
+}
+
+// Append: one warp per (token, K or V), a lane per 16-byte (or narrower) unit of
+// the token's kv_heads rows
+template <typename U>
+__global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, const int32_t* __restrict__ seqs,
+                                                const int32_t* __restrict__ starts, int n,
+                                                const char* __restrict__ k, long long k_token, long long k_head,
+                                                const char* __restrict__ v, long long v_token, long long v_head,
+                                                int tokens) {
+  const int lane = threadIdx.x & 31;
+  const int units = (int)(d.token_bytes / (long long)sizeof(U));
+  const long long head_bytes = d.token_bytes << d.page_shift;
+  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+  for (long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < 2ll * tokens; w += warps) {
+    const int t = (int)(w >> 1), side = (int)(w & 1);
+    int lo = 0, hi = n;                       // starts[lo] <= t < starts[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    const int s = seqs[lo], end = starts[lo + 1];
+    if (t < starts[lo] || t >= end || (unsigned)s >= (unsigned)d.max_seqs) {
+      if (lane == 0) set_status(d.status, MOE_KV_BAD_SEQ);
+      continue;
+    }
+    const long long pos = (long long)d.lens[s] - end + t;
+    const int col = (int)(pos >> d.page_shift);
+    const int p = pos < 0 || col >= d.max_pages ? -1 : d.table[(size_t)s * d.max_pages + col];
+    if ((unsigned)p >= (unsigned)d.num_pages) {
+      if (lane == 0) set_status(d.status, MOE_KV_BAD_PAGE);
+      continue;
+    }
+    char* to = (side ? d.v : d.k) + pool_off + p * (head_bytes * d.kv_heads) +
+               (pos & ((1 << d.page_shift) - 1)) * d.token_bytes;
+    const char* from = side ? v + t * v_token : k + t * k_token;
+    const long long from_head = side ? v_head : k_head;
+    for (int u = lane; u < units * d.kv_heads; u += 32) {
+      const int h = u / units, x = u - h * units;
+      reinterpret_cast<U*>(to + h * head_bytes)[x] = reinterpret_cast<const U*>(from + h * from_head)[x];
+    }
+  }
+}
+
+// Compaction, first launch (one block): U, the movers (list_a) and the holes
+// (list_b) in ascending order, the reference counts afterwards.
+__global__ void __launch_bounds__(kBookThreads) k_compact_plan(const Kv d, int32_t* refs_out, int32_t* used_out) {
+  const int t = threadIdx.x;
+  int used = 0;
+  for (int p0 = 0; p0 < d.num_pages; p0 += kBookThreads) {
+    const int p = p0 + t;
+    used += __syncthreads_count(p < d.num_pages && d.refs[p] > 0);
+  }
+  int movers = 0, holes = 0;
+  for (int p0 = 0; p0 < d.num_pages; p0 += kBookThreads) {
+    const int p = p0 + t;
+    const bool in = p < d.num_pages;
+    const bool busy = in && d.refs[p] > 0;
+    const int m = busy && p >= used, h = in && !busy && p < used;
+    int total;
+    const int at = block_scan(m | h << 16, &total);
+    if (m) d.list_a[movers + (at & 0xffff)] = p;
+    if (h) d.list_b[holes + (at >> 16)] = p;
+    movers += total & 0xffff, holes += total >> 16;
+  }
+  __syncthreads();
+  // a hole takes its mover's count (read before the mover's entry is cleared)
+  for (int i = t; i < movers; i += kBookThreads) refs_out[d.list_b[i]] = d.refs[d.list_a[i]];
+  __syncthreads();
+  for (int p = t; p < d.num_pages; p += kBookThreads) {
+    if (p >= used) refs_out[p] = 0;
+    else if (refs_out != d.refs && d.refs[p] > 0) refs_out[p] = d.refs[p];
+  }
+  if (t == 0) {
+    d.hdr[H_MOVES] = movers;
+    if (used_out) *used_out = used;
+  }
+}
+
+// Compaction, last launch: every table entry that names a mover names its hole
+// (the movers are ascending, so an entry is found by bisection)
+__global__ void __launch_bounds__(256) k_compact_table(const Kv d, int32_t* table_out) {
+  const int movers = d.hdr[H_MOVES];
+  const long long n = (long long)d.max_seqs * d.max_pages;
+  const int first = movers ? d.list_a[0] : 0x7fffffff;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    int p = d.table[i];
+    if (p >= first) {
+      int lo = 0, hi = movers;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (d.list_a[mid] <= p) lo = mid;
+        else hi = mid;
+      }
+      if (d.list_a[lo] == p) p = d.list_b[lo];
+    }
+    table_out[i] = p;
+  }
+}
+
+size_t bitmap_bytes(const moe_kv_pages& kv) { return ((size_t)kv.max_seqs + 31) / 32 * 4; }
+int rows_grid(int n) { return n < 1024 ? n : 1024; }
+
+}  // namespace
+
+size_t kv_work_bytes(const moe_kv_pages& kv) {
+  const size_t ints = kHdrInts + (size_t)kv.max_seqs * 5 + 1 + 2 * (size_t)kv.num_pages +
+                      (size_t)kv.max_seqs * kv.max_pages;
+  return (ints * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_kv_reserve(const moe_kv_pages& kv, const int32_t* seqs, const int32_t* counts, int n,
+                              cudaStream_t s) {
+  if (n <= 0) return cudaSuccess;
+  const Kv d = make(kv);
+  k_reserve<<<1, kBookThreads, 0, s>>>(d, seqs, counts, n);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)n * kv.layers * 2 * kv.kv_heads;
+  const int grid = device_sm_count() * 8;
+  k_copy_tails<<<most < grid ? (int)most : grid, 256, 0, s>>>(d);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const moe_kv_pages& kv, int layer, const int32_t* seqs, const int32_t* starts, int n,
+                             const void* k, long long k_token, long long k_head, const void* v, long long v_token,
+                             long long v_head, int tokens, cudaStream_t s) {
+  if (n <= 0 || tokens <= 0) return cudaSuccess;
+  const Kv d = make(kv);
+  const long long e = kv.dtype == MOE_BF16 ? 2 : 4;
+  const long long off = (long long)layer * kv.num_pages * kv.kv_heads * (d.token_bytes << d.page_shift);
+  const int most = device_sm_count() * 8;
+  const long long want = (2ll * tokens + 7) / 8;
+  const int grid = (int)(want < most ? want : most);
+  const bool wide = aligned(16, k, v, k_token * e, k_head * e, v_token * e, v_head * e);
+  if (wide)
+    k_append<uint4><<<grid, 256, 0, s>>>(d, off, seqs, starts, n, (const char*)k, k_token * e, k_head * e, (const char*)v,
+                                         v_token * e, v_head * e, tokens);
+  else
+    k_append<uint16_t><<<grid, 256, 0, s>>>(d, off, seqs, starts, n, (const char*)k, k_token * e, k_head * e,
+                                            (const char*)v, v_token * e, v_head * e, tokens);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_truncate(const moe_kv_pages& kv, const int32_t* seqs, const int32_t* lens, int n,
+                               cudaStream_t s) {
+  if (n <= 0) return cudaSuccess;
+  k_truncate<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(make(kv), seqs, lens, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_fork(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
+  if (n <= 0) return cudaSuccess;
+  const Kv d = make(kv);
+  k_fork_read<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(d, src, dst, n);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_fork_write<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(d, src, dst, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_copy(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
+  if (n <= 0) return cudaSuccess;
+  k_copy_pages<<<device_sm_count() * 8, 256, 0, s>>>(make(kv), src, dst, n, nullptr);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(const moe_kv_pages& kv, int32_t* table_out, int32_t* refs_out, int32_t* used,
+                              cudaStream_t s) {
+  const Kv d = make(kv);
+  k_compact_plan<<<1, kBookThreads, 0, s>>>(d, refs_out, used);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_copy_pages<<<device_sm_count() * 8, 256, 0, s>>>(d, d.list_a, d.list_b, 0, d.hdr + H_MOVES);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long n = (long long)kv.max_seqs * kv.max_pages;
+  const long long want = (n + 255) / 256;
+  const int most = device_sm_count() * 8;
+  k_compact_table<<<(int)(want < most ? want : most), 256, 0, s>>>(d, table_out);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

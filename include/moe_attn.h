@@ -1,0 +1,204 @@
+/*
+ * moe_attn.h -- the attention half of a decoder layer, part of libmoecache.so
+ *
+ * moe_cache.h serves a decoder layer's mixture of experts.  The entry points
+ * here are what runs next to it on the same GPU when a model is served: the
+ * norms that join the two halves, a paged key-value cache whose bookkeeping
+ * lives on the device, attention of one new token over those pages, and
+ * attention over whole packed prompts.
+ *
+ * Conventions are those of moe_cache.h: every function returns a moe_status
+ * and leaves its message in moe_cache_last_error(NULL); arguments are checked
+ * before any GPU work (MOE_EINVAL); pointers suffixed _d are device pointers
+ * and the caller owns every buffer; work is ordered on the caller's stream
+ * (NULL = legacy default stream) and nothing synchronises, so every call can
+ * be captured in a CUDA graph.  Nothing is allocated.
+ *
+ * Types: MOE_F32 or MOE_BF16, the two types of hidden states.  Sums, softmax
+ * statistics and norms are held in f32 whatever the type; outputs are rounded
+ * once.  (Prompt attention on the tensor cores also rounds each softmax weight
+ * to bf16 before its product with V.)
+ */
+#ifndef MOE_ATTN_H
+#define MOE_ATTN_H
+
+#include "moe_cache.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Limits checked at every call */
+#define MOE_ATTN_MAX_HEAD_DIM 256    /* head_dim: a multiple of 8 up to this */
+#define MOE_ATTN_MAX_GROUP 64        /* query heads per key head */
+#define MOE_NORM_MAX_HIDDEN 32768
+#define MOE_KV_MAX_SEQS 65536        /* rows of the page table */
+
+/* ------------------------------------------------------------------ norms */
+
+/* The join between a block (attention or experts) and the next one, per token:
+ *   n  = b * rsqrt(mean(b^2) + eps) * post_w     (n = b when post_w_d is NULL)
+ *   x' = x + res_scale * gate * n                (gate = 1 when gate_d is NULL)
+ *   y  = x' * rsqrt(mean(x'^2) + eps) * pre_w    (not computed when y_d is NULL)
+ * block_d = NULL: x' = x, the norm before a model's first block (post_w_d and
+ * gate_d must then be NULL).  x_out_d = NULL: x' is not stored.  y is computed
+ * from x' before x' is rounded.
+ * All tensors have the type `dtype`.  Rows are `hidden` contiguous elements;
+ * *_row is the distance between rows in elements (0 = the same row for every
+ * token; outputs need at least `hidden`).  gate_col = 1: one gate per channel
+ * of the row; 0: one gate per row (read at its first element).
+ * x_out_d may be x_d or block_d, y_d may be x_d or block_d (same row distance);
+ * other overlaps are not allowed. */
+typedef struct {
+  int dtype, hidden;
+  long long tokens;
+  const void* x_d;
+  const void* block_d;
+  const void* post_w_d;      /* [hidden] */
+  const void* gate_d;
+  const void* pre_w_d;       /* [hidden]; NULL only with y_d = NULL */
+  void* x_out_d;
+  void* y_d;
+  long long x_row, block_row, gate_row, x_out_row, y_row;
+  int gate_col;
+  float res_scale, eps;
+} moe_norm_args;
+
+moe_status moe_norm_residual(const moe_norm_args* a, moe_stream_t stream);
+
+/* ------------------------------------------------- paged key-value cache */
+
+/* One cache: `layers` layers that share one page table.  Token t of sequence s
+ * is at offset t % page_tokens of page table_d[s * max_pages + t / page_tokens]
+ * in every layer; K and V pools are
+ *   [layers][num_pages][kv_heads][page_tokens][head_dim].
+ * The caller owns and initialises the arrays: table -1, lens 0, refs 0, status
+ * 0, work 0 (pools may hold anything: tokens past a sequence's length are never
+ * used).  Entries past a sequence's last page are kept -1.
+ * refs_d[p] counts the table entries that name page p; 0 = free.
+ *
+ * The calls below change table, lens and refs on the device, in stream order.
+ * Lists of sequences are device arrays of at most max_seqs distinct rows.  A
+ * call whose device inputs are wrong, or that finds too few free pages, changes
+ * nothing, and the first such call since the status was zeroed leaves its
+ * reason in status_d; moe_kv_check reads it.
+ * Calls on one cache share work_d and must not overlap. */
+typedef struct {
+  int dtype;
+  int layers, kv_heads, head_dim;
+  int page_tokens;           /* a power of two, 1..1024 */
+  int num_pages, max_seqs, max_pages;
+  void* k_d;                 /* 16-byte aligned */
+  void* v_d;
+  int32_t* table_d;          /* [max_seqs, max_pages] */
+  int32_t* lens_d;           /* [max_seqs] tokens held */
+  int32_t* refs_d;           /* [num_pages] */
+  int32_t* status_d;         /* [1] */
+  void* work_d;              /* moe_kv_work_bytes, 256-byte aligned, zeroed once */
+  size_t work_bytes;
+} moe_kv_pages;
+
+/* status_d values */
+#define MOE_KV_OK 0
+#define MOE_KV_BAD_SEQ 1     /* a row outside [0, max_seqs), or twice in a list */
+#define MOE_KV_BAD_COUNT 2   /* a negative count or length */
+#define MOE_KV_TOO_LONG 3    /* more than max_pages pages in a row */
+#define MOE_KV_NO_PAGES 4    /* fewer free pages than the call needs */
+#define MOE_KV_BAD_PAGE 5    /* a page outside [0, num_pages) where a token should be */
+
+/* Bytes of work_d for a cache (only the counts and sizes of kv are read), used
+ * with attention of at most max_heads query heads. */
+moe_status moe_kv_work_bytes(const moe_kv_pages* kv, int max_heads, size_t* bytes);
+
+/* Make room for counts_d[i] more tokens in sequence seqs_d[i], i < n: lens grow
+ * and new pages, lowest free page first, go to the list's sequences in order
+ * (within one, in token order).  A partly filled last page that other rows
+ * share is replaced by a private copy of the tokens held (its place in the
+ * order comes before the sequence's new pages); every listed sequence that
+ * shares such a page gets its own. */
+moe_status moe_kv_reserve(const moe_kv_pages* kv, const int32_t* seqs_d, const int32_t* counts_d, int n,
+                          moe_stream_t stream);
+
+/* Write one layer's keys and values of the newest tokens: rows starts_d[i] ..
+ * starts_d[i + 1] of k_new / v_new [tokens, kv_heads, head_dim] are the last
+ * tokens of sequence seqs_d[i].  *_token / *_head: distances in elements between
+ * tokens and between heads (head_dim contiguous).  starts_d has n + 1 entries,
+ * ascending from 0 to `tokens`. */
+moe_status moe_kv_append(const moe_kv_pages* kv, int layer, const int32_t* seqs_d, const int32_t* starts_d, int n,
+                         const void* k_new_d, long long k_token, long long k_head, const void* v_new_d,
+                         long long v_token, long long v_head, int tokens, moe_stream_t stream);
+
+/* Keep the first min(lens, new_lens_d[i]) tokens of each listed sequence and
+ * release the pages past them (new_lens_d = NULL: keep none). */
+moe_status moe_kv_truncate(const moe_kv_pages* kv, const int32_t* seqs_d, const int32_t* new_lens_d, int n,
+                           moe_stream_t stream);
+
+/* Sequence dst_d[i] becomes a copy of src_d[i] that shares all its pages; what
+ * dst_d[i] held is released.  Every source is read as it was before the call,
+ * so one list can permute rows (dst distinct; src may repeat and may be in
+ * dst). */
+moe_status moe_kv_fork(const moe_kv_pages* kv, const int32_t* src_d, const int32_t* dst_d, int n,
+                       moe_stream_t stream);
+
+/* Copy whole pages dst_d[i] <- src_d[i] in every layer (no list entry may be
+ * both a source and a destination); table and refs are not touched. */
+moe_status moe_kv_copy(const moe_kv_pages* kv, const int32_t* src_d, const int32_t* dst_d, int n, moe_stream_t stream);
+
+/* Move the used pages to the front of the pool: with U pages in use, the i-th
+ * used page at or above U (ascending) moves to the i-th free page below U, in
+ * every layer.  The table and the reference counts that hold afterwards go to
+ * table_out_d and refs_out_d, which may be the cache's own arrays (then it is
+ * compacted in place) or others of their sizes (the cache's stay as they are,
+ * and remain valid until a page is reserved from the new ones).  used_d [1]
+ * receives U; it may be NULL. */
+moe_status moe_kv_compact(const moe_kv_pages* kv, int32_t* table_out_d, int32_t* refs_out_d, int32_t* used_d,
+                          moe_stream_t stream);
+
+/* Synchronise `stream` and report status_d: MOE_ESTATE with the reason if a call
+ * was refused on the device.  The status stays until the caller zeroes it. */
+moe_status moe_kv_check(const moe_kv_pages* kv, moe_stream_t stream);
+
+/* --------------------------------------------------------------- attention */
+
+/* One new token per sequence over the cache's pages: for query head h of list
+ * entry i, over the tokens t of sequence seqs_d[i] in [len - window, len)
+ * (window = 0: all),
+ *   s_t = scale * q . k_t,  m = max s_t,  out = sum exp(s_t - m) v_t / sum exp(s_t - m),
+ *   lse = m + log(sum exp(s_t - m)).
+ * Query head h reads key head h / (heads / kv_heads).  A sequence without
+ * tokens gives zeros, and lse = -inf.  The newest token's key and value are
+ * written (moe_kv_append) before the call.
+ * q_d [n, heads, head_dim] (distances q_token, q_head); out_d likewise;
+ * lse_d f32 [n, heads] or NULL.  Rows may repeat in seqs_d here.  A row or page
+ * out of range gives zeros for that entry and sets status_d. */
+moe_status moe_attn_decode(const moe_kv_pages* kv, int layer, const void* q_d, long long q_token, long long q_head,
+                           const int32_t* seqs_d, int n, int heads, float scale, int window, void* out_d,
+                           long long out_token, long long out_head, float* lse_d, moe_stream_t stream);
+
+/* Attention over whole prompts, packed one after the other.  Sequence i has
+ * queries starts_q_d[i] .. starts_q_d[i + 1] and keys starts_k_d[i] ..
+ * starts_k_d[i + 1] (its last keys are those of its queries; earlier ones come
+ * before them).  With lq queries and lk keys, query r sees the keys
+ *   j <= r + lk - lq,  and  j > r + lk - lq - window  when window > 0.
+ * A query that sees no key gives zeros, and lse = -inf.
+ * starts_*_d: n + 1 entries ascending from 0 to q_tokens / k_tokens. */
+typedef struct {
+  int dtype, heads, kv_heads, head_dim;
+  int n;                     /* sequences */
+  int q_tokens, k_tokens;
+  const int32_t* starts_q_d;
+  const int32_t* starts_k_d;
+  const void *q_d, *k_d, *v_d;
+  void* out_d;
+  float* lse_d;              /* [q_tokens, heads] or NULL */
+  long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+  float scale;
+  int window;
+} moe_prompt_args;
+
+moe_status moe_attn_prompt(const moe_prompt_args* a, moe_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MOE_ATTN_H */

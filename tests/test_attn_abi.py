@@ -1,0 +1,106 @@
+"""The structs of include/moe_attn.h and their ctypes bindings agree byte for
+byte, and wrong arguments are refused before any GPU work (no GPU needed)."""
+
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from tests.conftest import ROOT
+
+STRUCTS = ["moe_norm_args", "moe_kv_pages", "moe_prompt_args"]
+
+
+@pytest.fixture(scope="module")
+def abi():
+    from expert_slot_cache_topk_gb300 import _abi, _build
+    _build.build()
+    return _abi
+
+
+def test_struct_layouts_match_the_header(abi, tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "moe_attn.h"', "int main(void) {"]
+    for s in STRUCTS:
+        lines.append(f'  printf("{s} %zu\\n", sizeof({s}));')
+        lines += [f'  printf("{s}.{n} %zu\\n", offsetof({s}, {n}));' for n, _ in getattr(abi, s)._fields_]
+    src, exe = tmp_path / "p.c", tmp_path / "p"
+    src.write_text("\n".join(lines + ["  return 0;", "}"]) + "\n")
+    subprocess.check_call([cc, "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)])
+    facts = dict(line.split() for line in subprocess.check_output([str(exe)], text=True).splitlines())
+    for s in STRUCTS:
+        cls = getattr(abi, s)
+        assert ctypes.sizeof(cls) == int(facts[s])
+        for n, _ in cls._fields_:
+            assert getattr(cls, n).offset == int(facts[f"{s}.{n}"]), f"{s}.{n}"
+
+
+def cache(abi, **kw):
+    """A description with made-up (never followed) addresses."""
+    d = dict(dtype=abi.MOE_BF16, layers=2, kv_heads=4, head_dim=128, page_tokens=16, num_pages=100, max_seqs=8,
+             max_pages=50, k_d=4096, v_d=4096, table_d=4096, lens_d=4096, refs_d=4096, status_d=4096, work_d=4096,
+             work_bytes=1 << 30)
+    d.update(kw)
+    return abi.moe_kv_pages(**d)
+
+
+def refused(abi, status):
+    assert status == abi.MOE_EINVAL
+    assert abi.lib().moe_cache_last_error(None)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=2), dict(head_dim=12), dict(head_dim=264), dict(page_tokens=12),
+                                dict(page_tokens=0), dict(num_pages=0), dict(max_seqs=0), dict(max_pages=0),
+                                dict(layers=0), dict(k_d=None), dict(v_d=4098), dict(work_d=None), dict(work_d=4100),
+                                dict(work_bytes=64), dict(table_d=None), dict(status_d=4097), dict(max_pages=1 << 21)])
+def test_bad_caches_are_refused(abi, kw):
+    L, kv = abi.lib(), cache(abi, **kw)
+    refused(abi, L.moe_kv_reserve(kv, 4096, 4096, 1, None))
+    refused(abi, L.moe_kv_compact(kv, 4096, 4096, None, None))
+    refused(abi, L.moe_attn_decode(kv, 0, 4096, 512, 128, 4096, 1, 4, 1.0, 0, 4096, 512, 128, None, None))
+
+
+def test_bad_calls_are_refused(abi):
+    L, kv = abi.lib(), cache(abi)
+    refused(abi, L.moe_kv_reserve(kv, 4096, 4096, 9, None))          # more rows than the table has
+    refused(abi, L.moe_kv_reserve(kv, None, 4096, 1, None))
+    refused(abi, L.moe_kv_truncate(kv, None, None, 1, None))
+    refused(abi, L.moe_kv_fork(kv, 4096, None, 1, None))
+    refused(abi, L.moe_kv_copy(kv, 4096, 4096, 101, None))
+    refused(abi, L.moe_kv_append(kv, 2, 4096, 4096, 1, 4096, 512, 128, 4096, 512, 128, 1, None))
+    refused(abi, L.moe_kv_append(kv, 0, 4096, 4096, 1, 4097, 512, 128, 4096, 512, 128, 1, None))
+    refused(abi, L.moe_kv_append(kv, 0, 4096, 4096, 1, 4096, -1, 128, 4096, 512, 128, 1, None))
+    n = ctypes.c_size_t()
+    refused(abi, L.moe_kv_work_bytes(kv, 6, ctypes.byref(n)))        # heads not a multiple of kv_heads
+    refused(abi, L.moe_kv_work_bytes(kv, 4 * 65, ctypes.byref(n)))
+    assert L.moe_kv_work_bytes(kv, 32, ctypes.byref(n)) == abi.MOE_OK and n.value > 0
+
+    def decode(heads=8, scale=1.0, window=0, out_token=1024, out_head=128, layer=0, q=4096):
+        return L.moe_attn_decode(kv, layer, q, 1024, 128, 4096, 2, heads, scale, window, 4096, out_token, out_head, None,
+                                 None)
+    for kw in (dict(heads=6), dict(heads=0), dict(heads=4 * 65), dict(scale=float("nan")), dict(window=-1),
+               dict(out_head=64), dict(out_token=0), dict(layer=-1), dict(q=None), dict(q=4097)):
+        refused(abi, decode(**kw))
+
+
+def test_bad_prompts_and_norms_are_refused(abi):
+    L = abi.lib()
+    good = dict(dtype=abi.MOE_BF16, heads=8, kv_heads=4, head_dim=64, n=1, q_tokens=8, k_tokens=8, starts_q_d=4096,
+                starts_k_d=4096, q_d=4096, k_d=4096, v_d=4096, out_d=4096, lse_d=None, q_token=512, q_head=64,
+                k_token=256, k_head=64, v_token=256, v_head=64, out_token=512, out_head=64, scale=0.1, window=0)
+    for kw in (dict(dtype=7), dict(heads=6), dict(head_dim=20), dict(head_dim=512), dict(n=-1), dict(q_tokens=-1),
+               dict(window=-1), dict(scale=float("inf")), dict(q_d=None), dict(k_d=None), dict(starts_k_d=None),
+               dict(out_head=32), dict(out_token=0), dict(k_token=-1), dict(v_d=4097)):
+        refused(abi, L.moe_attn_prompt(abi.moe_prompt_args(**{**good, **kw}), None))
+    assert L.moe_attn_prompt(abi.moe_prompt_args(**{**good, "q_tokens": 0}), None) == abi.MOE_OK
+    norm = dict(dtype=abi.MOE_F32, hidden=64, tokens=2, x_d=4096, block_d=8192, post_w_d=None, gate_d=None, pre_w_d=4096,
+                x_out_d=4096, y_d=12288, x_row=64, block_row=64, gate_row=0, x_out_row=64, y_row=64, gate_col=0,
+                res_scale=1.0, eps=1e-6)
+    for kw in (dict(dtype=3), dict(hidden=0), dict(hidden=1 << 16), dict(tokens=-1), dict(eps=float("nan")),
+               dict(x_d=None), dict(pre_w_d=None), dict(x_out_d=None, y_d=None), dict(y_d=4096), dict(gate_col=2),
+               dict(block_d=None, post_w_d=4096), dict(y_row=63), dict(x_row=128), dict(x_d=4098), dict(x_row=-1)):
+        refused(abi, L.moe_norm_residual(abi.moe_norm_args(**{**norm, **kw}), None))

@@ -1,0 +1,582 @@
+"""The attention half of a decoder layer on the GPU, against float64: norms
+around a block, the page calls of the key-value cache, attention of one new
+token over pages, and attention over packed prompts."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests.attn_util import HostPages, assert_attn, attn_ref, ints, norm_ref, starts_of  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def A():
+    from expert_slot_cache_topk_gb300 import attention
+    return attention
+
+
+def randn(g, *shape, dtype=F32):
+    return torch.randn(*shape, generator=g, dtype=torch.float32).to(dtype).cuda()
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+# ------------------------------------------------------------------- norms
+
+def check_norm(got, ref, parts, dtype, what):
+    """bf16: one rounding (2^-8); f32: sums of squares over the row (at most 32768 terms pairwise by threads, far
+    below 1e-5 relative) and the sum x + s g n against the size of its parts."""
+    u = 2.0 ** -8 if dtype == BF else 1e-5
+    err = (got.double().cpu() - ref.cpu()).abs()
+    bound = u * ref.abs().cpu() + 1e-5 * parts.cpu()
+    assert (err <= bound).all(), f"{what}: worst {float((err - bound).max()):.3e}"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,hidden", [(1, 64), (3, 1), (2, 333), (5, 2048), (701, 2560), (7, 4104), (2, 16384),
+                                           (1, 32768), (3, 20001)])
+@pytest.mark.parametrize("gate,post", [("none", True), ("token", False), ("channel", True), ("full", True)])
+def test_norm_residual(A, dtype, tokens, hidden, gate, post):
+    g = gen(tokens * 7 + hidden)
+    x, b = randn(g, tokens, hidden, dtype=dtype), randn(g, tokens, hidden, dtype=dtype)
+    pre, pw = randn(g, hidden, dtype=dtype), randn(g, hidden, dtype=dtype) if post else None
+    gt = {"none": None, "token": (tokens, 1), "channel": (hidden,), "full": (tokens, hidden)}[gate]
+    gt = None if gt is None else randn(g, *gt, dtype=dtype)
+    xo, y = torch.empty_like(x), torch.empty_like(x)
+    A.norm_residual(x, b, pre, xo, y, post_weight=pw, gate=gt, res_scale=0.3, eps=1e-5)
+    rx, ry = norm_ref(x, b, pre, pw, gt, 0.3, 1e-5)
+    parts = x.double().abs() + (rx - x.double()).abs()
+    check_norm(xo, rx, parts, dtype, "x_out")
+    rms = torch.sqrt((rx * rx).mean(-1, keepdim=True) + 1e-5)
+    check_norm(y, ry, parts / rms * pre.double().abs(), dtype, "y")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_first_block_strided_and_in_place(A, dtype):
+    g = gen(3)
+    wide = randn(g, 37, 300, dtype=dtype)
+    x, pre = wide[:, 8:264], randn(g, 256, dtype=dtype)
+    y = torch.empty(37, 256, dtype=dtype, device="cuda")
+    A.norm_residual(x, pre_weight=pre, y=y)                      # no block: the norm alone
+    _, ry = norm_ref(x, None, pre, None, None, 1.0, 1e-6)
+    check_norm(y, ry, ry.abs(), dtype, "norm alone")
+    for lo in (0, 1):                                            # an offset that allows no wide loads
+        x, b = wide[:, lo:lo + 256], randn(g, 37, 256, dtype=dtype)
+        rx, ry = norm_ref(x, b, pre, pre, None, 0.5, 1e-6)
+        keep = wide.clone()
+        A.norm_residual(x, b, pre, x, b, post_weight=pre, res_scale=0.5)   # x_out over x, y over the block
+        check_norm(x, rx, 1 + rx.abs(), dtype, "in place x")
+        check_norm(b, ry, 1 + ry.abs(), dtype, "in place y")
+        outside = torch.ones(300, dtype=torch.bool)
+        outside[lo:lo + 256] = False
+        assert torch.equal(wide[:, outside.cuda()], keep[:, outside.cuda()])
+
+
+def test_norm_of_zeros_large_values_and_no_rows(A):
+    x = torch.zeros(2, 512, device="cuda")
+    x[1] = 1e18                                                  # mean of squares still fits f32
+    w, y = torch.ones(512, device="cuda"), torch.empty(2, 512, device="cuda")
+    A.norm_residual(x, pre_weight=w, y=y, eps=1e-6)
+    assert torch.equal(y[0], torch.zeros(512, device="cuda"))
+    assert (y[1] - 1).abs().max() < 1e-6
+    A.norm_residual(x[:0], pre_weight=w, y=y[:0])
+
+
+def test_norm_refusals(A):
+    from expert_slot_cache_topk_gb300._abi import MoeError
+    x, w = torch.zeros(2, 64, device="cuda"), torch.ones(64, device="cuda")
+    y = torch.empty_like(x)
+    with pytest.raises(MoeError):
+        A.norm_residual(x, pre_weight=w)                         # no output
+    with pytest.raises(MoeError):
+        A.norm_residual(x, y=y)                                  # y without its weight
+    with pytest.raises(MoeError):
+        A.norm_residual(x, pre_weight=w, y=y, post_weight=w)     # post_weight without a block
+    with pytest.raises(MoeError):
+        A.norm_residual(x, x, w, y, y)                           # one buffer for both outputs
+    with pytest.raises(MoeError):
+        A.norm_residual(x, pre_weight=w, y=y, eps=-1.0)
+    with pytest.raises(TypeError):
+        A.norm_residual(x.half(), pre_weight=w, y=y)
+    with pytest.raises(TypeError):
+        A.norm_residual(x, x.to(BF), w, y)
+    with pytest.raises(ValueError):
+        A.norm_residual(x, x, w, y, gate=torch.ones(3, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        A.norm_residual(x.t(), pre_weight=w, y=y)
+
+
+# ------------------------------------------------------------------- pages
+
+def new_cache(A, dtype=BF, layers=2, kv_heads=2, dim=64, page=16, pages=40, seqs=8, cols=12, seed=5, poison=False,
+              max_heads=None):
+    kv = A.KVPages.empty(layers, kv_heads, dim, page, pages, seqs, cols, dtype=dtype, max_heads=max_heads)
+    g = gen(seed)
+    for t in (kv.k, kv.v):
+        t.copy_(torch.full_like(t, math.nan) if poison else randn(g, *t.shape, dtype=dtype))
+    return kv, HostPages(pages, seqs, cols, page)
+
+
+def assert_state(kv, host):
+    assert np.array_equal(kv.table.cpu().numpy(), host.table)
+    assert np.array_equal(kv.lens.cpu().numpy(), host.lens)
+    assert np.array_equal(kv.refs.cpu().numpy(), host.refs)
+
+
+def bits(t):
+    return t.view(torch.int16 if t.dtype == BF else torch.int32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page", [1, 16, 64])
+def test_page_calls_follow_the_host_model(A, dtype, page):
+    """A random run of every call; tables, lengths and counts after each, and the tokens of every sequence."""
+    rng = np.random.default_rng(page)
+    layers, kv_heads, dim, pages, seqs, cols = 2, 3, 24, 64, 9, 20
+    kv, host = new_cache(A, dtype, layers, kv_heads, dim, page, pages, seqs, cols)
+    token = {s: [] for s in range(seqs)}                        # the values each sequence should hold
+    serial = 0
+    for step in range(60):
+        what = rng.choice(["reserve", "reserve", "truncate", "fork", "compact", "free"])
+        n = int(rng.integers(1, seqs + 1))
+        rows = rng.permutation(seqs)[:n]
+        if what == "reserve":
+            counts = rng.integers(0, 2 * page + 3, n)
+            copies = host.reserve(rows, counts)
+            kv.reserve(ints(rows), ints(counts))
+            if copies is None:
+                with pytest.raises(Exception):
+                    kv.check()
+                kv.status.zero_()
+                assert_state(kv, host)
+                continue
+            T = int(counts.sum())
+            for layer in range(layers):
+                vals = torch.arange(T, dtype=torch.float32)[:, None, None] + serial + \
+                    torch.arange(kv_heads)[None, :, None] * 0.25
+                k = vals.expand(T, kv_heads, dim).contiguous().to(dtype).cuda()
+                kv.append(layer, ints(rows), starts_of(counts), k, -k)
+            at = 0
+            for s, c in zip(rows, counts):
+                token[s] += [serial + at + j for j in range(c)]
+                at += int(c)
+            serial = (serial + T) % 40                           # small numbers: exact in bf16
+        elif what == "truncate":
+            lens = rng.integers(0, 3 * page + 1, n)
+            host.truncate(rows, lens)
+            kv.truncate(ints(rows), ints(lens))
+            for s, c in zip(rows, lens):
+                token[s] = token[s][:c]
+        elif what == "free":
+            host.truncate(rows[:1], [0])
+            kv.free(ints(rows[:1]))
+            token[rows[0]] = []
+        elif what == "fork":
+            src = rng.integers(0, seqs, n)
+            host.fork(src, rows)
+            kv.fork(ints(src), ints(rows))
+            old = {s: list(token[s]) for s in range(seqs)}
+            for a, b in zip(src, rows):
+                token[b] = list(old[a])
+        else:
+            _, used = host.compact()
+            u = ints([0])
+            kv.compact(used=u)
+            assert int(u) == used
+        kv.check()
+        assert_state(kv, host)
+    table, lens = kv.table.cpu().numpy(), kv.lens.cpu().numpy()
+    k, v = kv.k.float().cpu(), kv.v.float().cpu()
+    for s in range(seqs):
+        assert lens[s] == len(token[s])
+        for t, val in enumerate(token[s]):
+            p, o = table[s, t // page], t % page
+            want = torch.tensor(float(val)) + torch.arange(kv_heads) * 0.25
+            want = want.to(dtype).float()
+            for layer in range(layers):
+                assert torch.equal(k[layer, p, :, o, 0], want) and torch.equal(v[layer, p, :, o, dim - 1], -want)
+
+
+def test_reserve_copies_only_the_tokens_held_and_shares_nothing(A):
+    kv, host = new_cache(A, page=16, pages=30)
+    kv.reserve(ints([0]), ints([21]))
+    host.reserve([0], [21])
+    kv.fork(ints([0, 0]), ints([3, 5]))
+    host.fork([0, 0], [3, 5])
+    before_k = kv.k.clone()
+    copies = host.reserve([5, 0, 3], [1, 1, 0])
+    kv.reserve(ints([5, 0, 3]), ints([1, 1, 0]))
+    kv.check()
+    assert_state(kv, host)
+    assert len(copies) == 2 and len({c[1] for c in copies}) == 2
+    for old, new, held in copies:
+        assert held == 5
+        assert torch.equal(bits(kv.k[:, new, :, :held]), bits(before_k[:, old, :, :held]))
+        assert torch.equal(bits(kv.k[:, new, :, held:]), bits(before_k[:, new, :, held:]))
+
+
+def test_compact_out_of_place_keeps_the_old_table(A):
+    rng = np.random.default_rng(0)
+    kv, host = new_cache(A, pages=80, seqs=8, cols=12)
+    lens = rng.integers(20, 150, 8)
+    kv.reserve(ints(range(8)), ints(lens))
+    host.reserve(range(8), lens)
+    kv.fork(ints([2]), ints([6]))
+    host.fork([2], [6])
+    kv.free(ints([0, 3]))
+    host.truncate([0, 3], [0, 0])
+    table, refs, pool = kv.table.clone(), kv.refs.clone(), kv.k.clone()
+    t_out, r_out, used = torch.empty_like(table), torch.empty_like(refs), ints([0])
+    for _ in range(2):                                            # the old table still holds, so twice is the same
+        kv.compact(t_out, r_out, used)
+    assert torch.equal(kv.table, table) and torch.equal(kv.refs, refs)
+    moved, n = host.compact()
+    assert int(used) == n and moved
+    assert np.array_equal(t_out.cpu().numpy(), host.table) and np.array_equal(r_out.cpu().numpy(), host.refs)
+    for a, b in moved.items():
+        assert torch.equal(bits(kv.k[:, b]), bits(pool[:, a]))
+
+
+def test_copy_pages(A):
+    kv, _ = new_cache(A, layers=3, pages=20)
+    k, v = kv.k.clone(), kv.v.clone()
+    kv.copy(ints([1, 7, 19]), ints([0, 3, 4]))
+    k[:, [0, 3, 4]], v[:, [0, 3, 4]] = k[:, [1, 7, 19]], v[:, [1, 7, 19]]
+    assert torch.equal(bits(kv.k), bits(k)) and torch.equal(bits(kv.v), bits(v))
+
+
+@pytest.mark.parametrize("call,code", [
+    (lambda kv: kv.reserve(ints([0, 0]), ints([1, 1])), "twice"),
+    (lambda kv: kv.reserve(ints([8]), ints([1])), "out of range"),
+    (lambda kv: kv.reserve(ints([-1]), ints([1])), "out of range"),
+    (lambda kv: kv.reserve(ints([1]), ints([-1])), "negative"),
+    (lambda kv: kv.reserve(ints([1]), ints([12 * 16 + 1])), "longer"),
+    (lambda kv: kv.reserve(ints([1, 2, 3, 4]), ints([190] * 4)), "longer"),
+    (lambda kv: kv.reserve(ints([1, 3, 4, 5]), ints([190] * 4)), "free pages"),
+    (lambda kv: kv.truncate(ints([2, 2]), ints([0, 0])), "twice"),
+    (lambda kv: kv.truncate(ints([2]), ints([-3])), "negative"),
+    (lambda kv: kv.free(ints([99])), "out of range"),
+    (lambda kv: kv.fork(ints([0, 0]), ints([1, 1])), "twice"),
+    (lambda kv: kv.fork(ints([77]), ints([1])), "out of range"),
+    (lambda kv: kv.copy(ints([40]), ints([1])), "no valid page"),
+])
+def test_wrong_device_lists_change_nothing(A, call, code):
+    from expert_slot_cache_topk_gb300._abi import MOE_ESTATE, MoeError
+    kv, host = new_cache(A)
+    kv.reserve(ints([0, 2]), ints([30, 50]))
+    host.reserve([0, 2], [30, 50])
+    kv.check()
+    k = kv.k.clone()
+    call(kv)
+    with pytest.raises(MoeError) as e:
+        kv.check()
+    assert e.value.status == MOE_ESTATE and code in str(e.value)
+    assert_state(kv, host)
+    assert torch.equal(bits(kv.k), bits(k))
+    kv.status.zero_()
+    kv.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_from_strided_and_unaligned_rows(A, dtype):
+    kv, _ = new_cache(A, dtype, kv_heads=2, dim=40)
+    g = gen(8)
+    counts = [3, 0, 17]
+    kv.reserve(ints([4, 1, 6]), ints(counts))
+    for lo in (0, 8, 1):                                          # inside a wider projection's output
+        wide = randn(g, 20, 300, dtype=dtype)
+        k = wide[:, lo:lo + 80].unflatten(1, (2, 40))
+        v = wide[:, lo + 100:lo + 180].unflatten(1, (2, 40))
+        kv.append(1, ints([4, 1, 6]), starts_of(counts), k, v)
+        kv.check()
+        table = kv.table.cpu()
+        for s, first, n in ((4, 0, 3), (6, 3, 17)):
+            for t in range(n):
+                assert torch.equal(bits(kv.k[1, table[s, t // 16], :, t % 16]), bits(k[first + t]))
+                assert torch.equal(bits(kv.v[1, table[s, t // 16], :, t % 16]), bits(v[first + t]))
+
+
+# ------------------------------------------------------------------ decode
+
+def fill(A, lens, dtype, kv_heads, dim, page, seed, poison=True, max_heads=None):
+    """A cache whose sequences hold random tokens, pages in a scrambled order; everything else is NaN."""
+    cols = max(1, max(-(-n // page) for n in lens))
+    pages = sum(-(-n // page) for n in lens) + 5
+    kv = A.KVPages.empty(2, kv_heads, dim, page, pages, len(lens), cols, dtype=dtype, max_heads=max_heads)
+    g = gen(seed)
+    for t in (kv.k, kv.v):
+        t.fill_(math.nan if poison else 0.0)
+    perm = torch.randperm(pages, generator=g).to(torch.int32)
+    table, at = torch.full((len(lens), cols), -1, dtype=torch.int32), 0
+    keys, values = [], []
+    kc, vc = kv.k.cpu(), kv.v.cpu()
+    for s, n in enumerate(lens):
+        have = -(-n // page)
+        table[s, :have] = perm[at:at + have]
+        at += have
+        k = torch.randn(n, kv_heads, dim, generator=g).to(dtype)
+        v = torch.randn(n, kv_heads, dim, generator=g).to(dtype)
+        keys.append(k)
+        values.append(v)
+        pos = torch.arange(n)
+        pg = table[s, pos // page].long()
+        kc[1, pg, :, pos % page] = k
+        vc[1, pg, :, pos % page] = v
+    kv.k.copy_(kc)
+    kv.v.copy_(vc)
+    kv.table.copy_(table)
+    kv.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    return kv, keys, values, g
+
+
+DECODE = [
+    # lens, heads, kv_heads, dim, page, window
+    ([1], 1, 1, 64, 16, 0),
+    ([0, 5, 17, 16, 15, 33], 4, 2, 128, 16, 0),
+    ([1000, 0, 1, 257], 16, 16, 128, 64, 0),
+    ([513, 2049], 20, 4, 128, 32, 0),
+    ([300, 77, 4000], 32, 4, 64, 16, 0),
+    ([9000], 16, 1, 128, 16, 0),
+    ([700, 3], 34, 2, 128, 16, 0),
+    ([130, 64, 5], 8, 8, 64, 64, 50),
+    ([1025, 31, 0], 8, 2, 128, 16, 1),
+    ([900, 1200], 10, 2, 128, 16, 333),
+    ([200, 31], 6, 3, 80, 16, 0),
+    ([90, 310], 4, 2, 8, 4, 0),
+    ([150], 4, 1, 256, 16, 0),
+    ([150, 41], 6, 2, 200, 1, 0),
+    ([12] * 70, 8, 2, 64, 16, 0),
+    ([2100, 40], 64, 1, 64, 1024, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,heads,kv_heads,dim,page,window", DECODE)
+def test_decode(A, dtype, lens, heads, kv_heads, dim, page, window):
+    kv, keys, values, g = fill(A, lens, dtype, kv_heads, dim, page, len(lens) + heads)
+    order = torch.randperm(len(lens), generator=g).tolist()
+    if len(order) > 1:
+        order.append(order[0])                                    # a row may repeat
+    q = randn(g, len(order), heads, dim, dtype=dtype)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((len(order), heads), 7.0, device="cuda")
+    kv.attend(1, q, ints(order), out, window=window, lse=lse)
+    kv.check()
+    for i, s in enumerate(order):
+        ro, rl = attn_ref(q[i:i + 1], keys[s], values[s], dim ** -0.5, window)
+        vmax = float(values[s].double().abs().max()) if lens[s] else 0.0
+        assert_attn(out[i:i + 1], lse[i:i + 1], ro, rl, vmax, f"row {i} of length {lens[s]}")
+    again = torch.empty_like(out)
+    for _ in range(3):                                            # the same bits every time, without lse too
+        kv.attend(1, q, ints(order), again, window=window)
+        assert torch.equal(bits(again), bits(out))
+
+
+def test_decode_strides_streams_and_graph(A):
+    kv, keys, values, g = fill(A, [100, 700], BF, 2, 128, 16, 3)
+    wide = randn(g, 2, 8 * 128 + 24, dtype=BF)
+    s = torch.cuda.Stream()
+    for lo in (0, 8, 3):
+        q = wide[:, lo:lo + 8 * 128].unflatten(1, (8, 128))
+        out = torch.zeros(2, 8, 300, dtype=BF, device="cuda")[:, :, lo:lo + 128]
+        seqs = ints([1, 0])
+        s.wait_stream(torch.cuda.current_stream())
+        kv.attend(1, q, seqs, out, stream=s)
+        s.synchronize()
+        for i, r in enumerate((1, 0)):
+            ro, _ = attn_ref(q[i:i + 1], keys[r], values[r], 128 ** -0.5)
+            assert_attn(out[i:i + 1], None, ro, None, float(values[r].double().abs().max()), f"offset {lo}")
+    q, out, seqs = wide[:, :1024].unflatten(1, (8, 128)), torch.empty(2, 8, 128, dtype=BF, device="cuda"), ints([0, 1])
+    kv.attend(1, q, seqs, out)
+    want = out.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        kv.attend(1, q, seqs, out, stream=s)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), bits(want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heads", [2, 8])
+def test_decode_extreme_scores(A, dtype, heads):
+    """Scores of +-1e4 (one token takes everything), -inf in a key, and NaN in one sequence only."""
+    kv, keys, values, g = fill(A, [600, 40, 40], dtype, 2, 64, 16, 4)
+    q = randn(g, 3, heads, 64, dtype=dtype)
+    out = torch.empty_like(q)
+    kv.attend(1, q, ints([0, 1, 2]), out, scale=1000.0)
+    for i in range(3):
+        ro, _ = attn_ref(q[i:i + 1], keys[i], values[i], 1000.0)
+        s = torch.einsum("hd,jhd->hj", q[i].double().cpu(), keys[i].double().repeat_interleave(heads // 2, 1)) * 1000
+        top = s.topk(2, 1).values
+        sure = (top[:, 0] - top[:, 1]) > 50                       # elsewhere f32 scores may order two tokens otherwise
+        err = (out[i].double().cpu() - ro[0]).abs().amax(1)
+        assert (err[sure] <= 2.0 ** -7 * float(values[i].double().abs().max())).all()
+    page = int(kv.table[1, 0])
+    kv.v[1, page, 0, 3, 5] = math.nan
+    kv.attend(1, q, ints([0, 1, 2]), out)
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2]).all()
+    assert torch.isnan(out[1, :heads // 2, 5]).all()
+    assert torch.isfinite(out[1, heads // 2:]).all()
+
+
+def test_decode_bad_rows_and_pages_give_zeros(A):
+    from expert_slot_cache_topk_gb300._abi import MoeError
+    kv, keys, values, g = fill(A, [100, 60], BF, 2, 64, 16, 6)
+    q = randn(g, 2, 4, 64, dtype=BF)
+    out = torch.ones_like(q)
+    kv.attend(1, q, ints([5, 0]), out)
+    with pytest.raises(MoeError):
+        kv.check()
+    assert not out[0].any() and out[1].any()
+
+
+def test_decode_refusals(A):
+    from expert_slot_cache_topk_gb300._abi import MoeError
+    kv, *_ = fill(A, [20], BF, 2, 64, 16, 6)
+    q = torch.zeros(1, 4, 64, dtype=BF, device="cuda")
+    out = torch.empty_like(q)
+    with pytest.raises(MoeError):
+        kv.attend(2, q, ints([0]), out)                           # layer
+    with pytest.raises(MoeError):
+        kv.attend(1, q[:, :3], ints([0]), out[:, :3])             # heads not a multiple of kv_heads
+    with pytest.raises(MoeError):
+        kv.attend(1, q, ints([0]), out, window=-1)
+    with pytest.raises(MoeError):
+        kv.attend(1, q, ints([0]), out, scale=math.inf)
+    with pytest.raises(TypeError):
+        kv.attend(1, q.float(), ints([0]), out)
+    with pytest.raises(TypeError):
+        kv.attend(1, q, torch.zeros(1, dtype=torch.int64, device="cuda"), out)
+    with pytest.raises(ValueError):
+        kv.attend(1, q[:, :, :32], ints([0]), out[:, :, :32])
+    with pytest.raises(TypeError):
+        kv.attend(1, q, ints([0]), out, lse=torch.zeros(1, 4, dtype=torch.float64, device="cuda"))
+    with pytest.raises(MoeError):
+        A.KVPages.empty(1, 1, 12, 16, 4, 1, 1)                    # head_dim
+    with pytest.raises(MoeError):
+        A.KVPages.empty(1, 1, 16, 12, 4, 1, 1)                    # page size
+
+
+# ------------------------------------------------------------------ prompt
+
+PROMPT = [
+    # (lq, lk) pairs, heads, kv_heads, dim, window
+    ([(1, 1)], 1, 1, 64, 0),
+    ([(5, 5), (0, 0), (1, 1), (130, 130), (64, 64)], 4, 2, 128, 0),
+    ([(257, 257)], 2, 2, 128, 0),
+    ([(300, 300), (511, 511)], 5, 1, 64, 0),
+    ([(100, 400), (1, 259), (128, 128 + 128)], 8, 2, 128, 0),
+    ([(40, 7), (3, 0), (0, 9), (200, 150)], 4, 4, 64, 0),          # more queries than keys: the first see nothing
+    ([(400, 400), (65, 300)], 4, 2, 128, 100),
+    ([(300, 300)], 2, 1, 64, 1),
+    ([(150, 150), (33, 40)], 4, 2, 80, 0),
+    ([(90, 90)], 4, 2, 8, 0),
+    ([(140, 170)], 2, 1, 256, 60),
+    ([(700, 1100), (1, 1), (2, 2), (3, 3)], 16, 2, 128, 0),
+]
+
+
+def prompt_inputs(g, lens, heads, kv_heads, dim, dtype):
+    Tq, Tk = sum(a for a, _ in lens), sum(b for _, b in lens)
+    return (randn(g, Tq, heads, dim, dtype=dtype), randn(g, Tk, kv_heads, dim, dtype=dtype),
+            randn(g, Tk, kv_heads, dim, dtype=dtype), starts_of([a for a, _ in lens]), starts_of([b for _, b in lens]))
+
+
+def check_prompt(q, k, v, lens, out, lse, scale, window, what=""):
+    a = b = 0
+    for lq, lk in lens:
+        ro, rl = attn_ref(q[a:a + lq], k[b:b + lk], v[b:b + lk], scale, window)
+        vmax = float(v[b:b + lk].double().abs().max()) if lk else 0.0
+        assert_attn(out[a:a + lq], None if lse is None else lse[a:a + lq], ro, rl, vmax, f"{what} ({lq}, {lk})")
+        a, b = a + lq, b + lk
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,heads,kv_heads,dim,window", PROMPT)
+def test_prompt(A, dtype, lens, heads, kv_heads, dim, window):
+    g = gen(heads + dim)
+    q, k, v, sq, sk = prompt_inputs(g, lens, heads, kv_heads, dim, dtype)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    A.attn_prompt(q, k, v, sq, sk, out, window=window, lse=lse)
+    check_prompt(q, k, v, lens, out, lse, dim ** -0.5, window)
+    again = torch.empty_like(out)
+    A.attn_prompt(q, k, v, sq, sk, again, window=window)
+    assert torch.equal(bits(again), bits(out))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lo", [0, 8, 1])
+def test_prompt_inside_a_fused_projection(A, dtype, lo):
+    """q, k and v as columns of one projection's output, at offsets that allow wide loads or do not."""
+    g = gen(lo)
+    T, dim = 200, 64
+    wide = randn(g, T, (4 + 2 + 2) * dim + 16, dtype=dtype)
+    q = wide[:, lo:lo + 4 * dim].unflatten(1, (4, dim))
+    k = wide[:, lo + 4 * dim:lo + 6 * dim].unflatten(1, (2, dim))
+    v = wide[:, lo + 6 * dim:lo + 8 * dim].unflatten(1, (2, dim))
+    out = torch.zeros(4, T, dim, dtype=dtype, device="cuda").transpose(0, 1)
+    st = starts_of([130, 70])
+    A.attn_prompt(q, k, v, st, st, out)
+    check_prompt(q, k, v, [(130, 130), (70, 70)], out, None, dim ** -0.5, 0, f"offset {lo}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_values_behind_the_mask_do_not_matter(A, dtype, bad, dim):
+    """A key or value that is not finite touches the queries that see it and no others: not the earlier queries
+    of its sequence, nor the neighbours packed around it, nor queries past the window."""
+    g = gen(1)
+    lens = [(70, 70), (300, 300), (90, 90)]
+    q, k, v, sq, sk = prompt_inputs(g, lens, 4, 2, dim, dtype)
+    clean = torch.empty_like(q)
+    A.attn_prompt(q, k, v, sq, sk, clean, window=120)
+    at = 70 + 150
+    v[at, 0] = bad
+    k[at, 1] = math.nan
+    out = torch.empty_like(q)
+    A.attn_prompt(q, k, v, sq, sk, out, window=120)
+    hit = torch.zeros(q.shape[0], dtype=torch.bool)
+    hit[at:at + 120] = True
+    assert torch.equal(bits(out[~hit]), bits(clean[~hit]))
+    assert not torch.isfinite(out[hit]).any()
+
+
+def test_prompt_refusals(A):
+    from expert_slot_cache_topk_gb300._abi import MoeError
+    q = torch.zeros(4, 4, 64, dtype=BF, device="cuda")
+    k = torch.zeros(4, 2, 64, dtype=BF, device="cuda")
+    out, st = torch.empty_like(q), ints([0, 4])
+    with pytest.raises(MoeError):
+        A.attn_prompt(q[:, :3], k, k, st, st, out[:, :3])
+    with pytest.raises(MoeError):
+        A.attn_prompt(q, k, k, st, st, out, window=-2)
+    with pytest.raises(MoeError):
+        A.attn_prompt(q, k, k, st, st, out, scale=math.nan)
+    with pytest.raises(MoeError):
+        A.attn_prompt(q[..., :12], k[..., :12], k[..., :12], st, st, out[..., :12])
+    with pytest.raises(TypeError):
+        A.attn_prompt(q, k.float(), k, st, st, out)
+    with pytest.raises(TypeError):
+        A.attn_prompt(q, k, k, st.long(), st, out)
+    with pytest.raises(TypeError):
+        A.attn_prompt(q, k, k, st, ints([0, 2, 4]), out)
+    with pytest.raises(ValueError):
+        A.attn_prompt(q, k, k[:3], st, st, out)
+    with pytest.raises(ValueError):
+        A.attn_prompt(q, k, k, st, st, out.transpose(1, 2).contiguous().transpose(1, 2))
+    A.attn_prompt(q[:0], k[:0], k[:0], ints([0, 0]), ints([0, 0]), out[:0])      # no tokens
