@@ -14,6 +14,8 @@
 
 namespace moe {
 
+cudaError_t launch_attn_prompt_tc(const moe_prompt_args& a, cudaStream_t s);   // k_attn_prompt_tc.cu
+
 namespace {
 
 using namespace attn;
@@ -246,6 +248,8 @@ cudaError_t by_dim(const moe_prompt_args& a, cudaStream_t s) {
 
 cudaError_t launch_attn_prompt(const moe_prompt_args& a, cudaStream_t s) {
   if (a.n <= 0 || a.q_tokens <= 0) return cudaSuccess;
+  const cudaError_t tc = launch_attn_prompt_tc(a, s);
+  if (tc != cudaErrorNotSupported) return tc;
   const long long e = a.dtype == MOE_BF16 ? 2 : 4;
   const bool vec = aligned(16, a.q_d, a.k_d, a.v_d, a.q_token * e, a.q_head * e, a.k_token * e, a.k_head * e,
                            a.v_token * e, a.v_head * e);

@@ -1,0 +1,624 @@
+// Attention over packed bf16 prompts on the tensor cores (head_dim up to 128).
+//
+// A block takes 256 queries of one head as two tiles of 128 rows.  Per tile and
+// 128 keys:  S = Q K^T (f32 in tensor memory);  one thread per row reads its
+// 128 scores, p = 2^(s scale log2e - m) with a running maximum m, and writes p
+// back as bf16 over the scores;  O += P V with P read from tensor memory.
+//
+// Warp roles (12 warps, one block per SM):
+//   warps 0-3, 4-7   softmax of tile 0 / tile 1: thread = row = tensor-memory lane;
+//                    at the end they scale O by 1 / l and store it (register
+//                    split: 208 each, the other four warps 88);
+//   warp 8           issues every tcgen05.mma:  PV0(j) S0(j+1) PV1(j) S1(j+1), so
+//                    the tensor cores work on one tile while the other's softmax
+//                    runs;  warp 9 loads Q, K and V by TMA (128-byte swizzle);
+//   warps 10, 11     clean the values of steps that a mask crosses (below).
+// Tensor memory, 512 columns: S0 S1 (128 each, P over the first half of each)
+// and O0 O1.  MMAs execute in the order of issue, so S(j+1) may overwrite P(j)
+// right after PV(j), and a commit after S(j+1) also says that PV(j) is done.
+//
+// The running maximum is lazy: m grows only when a row's maximum exceeds it by
+// more than 8 (weights then stay below 2^8, exact in the same relative
+// precision), so O is rescaled a few times per row at most; that happens in
+// tensor memory between S(j) and PV(j), when no MMA touches O.
+//
+// Masks: only tiles that the causal diagonal, the window or the sequence's end
+// crosses are masked (scores become -inf).  A weight of 0 times a value that is
+// not finite would still give NaN, so in those steps two warps zero, in shared
+// memory, the values past the sequence's end and every value that is not finite;
+// the rows that do see such a value are computed again with plain arithmetic
+// that never touches hidden keys (redo_row).  Other rows keep their bits.
+#include <cuda.h>
+#include <cmath>
+
+#include "attn_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace attn;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kRows = 128;                      // queries per tile
+constexpr int kKeys = 128;                      // keys per step
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kCleanWarp = 10, kTcThreads = 384;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 x 208 + 128 x 88 = 384 x 168, the launch's total
+constexpr float kSlack = 8.f;                   // how far (log2) weights may exceed 1 before O is rescaled
+constexpr unsigned long long kLimitNs = 2000000000ull;   // bound of every wait
+
+template <int DP>
+struct Shape {
+  static constexpr int kBox = 128 * 128;                   // bytes of 128 rows x 64 bf16
+  static constexpr int kTile = kBox * (DP / 64);           // 128 rows x DP
+  static constexpr int kRing = DP == 128 ? 5 : 8;          // K / V tiles in flight
+  static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
+};
+
+struct PromptTc {
+  const int32_t *starts_q, *starts_k;
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* out;
+  float* lse;
+  long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+  int n, q_tokens, k_tokens, heads, group, D, window, slots;
+  float scale;
+};
+
+struct Ctl {
+  unsigned long long qfull[2], kvfull[8], kvempty[8], sfull[2], pfull[2], ofull[2], vgo, vclean;
+  uint32_t tmem;
+  int stop;
+  int bad_lo, bad_hi;            // keys (of the sequence) with a value that was zeroed: first, last
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_tx(uint32_t bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Rows of 128 bytes in the 128-byte swizzle, 8-row groups 1024 bytes apart.
+// K-major (Q, K): rows are the M / N index, 64 columns of the contraction.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// N-major (V): rows are the contraction index (keys), 64 columns of N per box;
+// the next 64 columns are a box (16 KB) further: the leading byte offset.
+__device__ __forceinline__ uint64_t desc_n(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(16384 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// 32 columns without the wait; tie() afterwards, once the wait is done
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// arithmetic on r stays behind the statements before this one
+__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// false once a wait of the block has run out
+__device__ __forceinline__ bool wait_for(Ctl& c, unsigned long long& bar, unsigned parity) {
+  const uint32_t b = tc::smem_u32(&bar);
+  if (tc::mbar_try(b, parity)) return true;
+  if (*reinterpret_cast<volatile int*>(&c.stop)) return false;
+  if (tc::mbar_wait(b, parity, kLimitNs)) return true;
+  *reinterpret_cast<volatile int*>(&c.stop) = 1;
+  return false;
+}
+
+// the whole warp waits and goes on, or stops, together
+__device__ __forceinline__ bool warp_wait(Ctl& c, unsigned long long& bar, unsigned parity) {
+  return __all_sync(kAll, wait_for(c, bar, parity));
+}
+
+// What a tile of 128 rows has to do: the steps [first, last) of 128 keys
+struct Tile {
+  int r0, first, last;
+};
+
+// One row again, by one warp: only the keys that the row sees are read
+__device__ __noinline__ void redo_row(const PromptTc& a, int h, int q_at, long long k_first, int count) {
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat16* q = a.q + q_at * a.q_token + h * a.q_head;
+  const __nv_bfloat16* k = a.k + k_first * a.k_token + (long long)(h / a.group) * a.k_head;
+  const __nv_bfloat16* v = a.v + k_first * a.v_token + (long long)(h / a.group) * a.v_head;
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < count; j0 += 32) {
+    float s = -INFINITY;
+    if (j0 + lane < count) {
+      s = 0.f;
+      for (int d = 0; d < a.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[(j0 + lane) * a.k_token + d]), s);
+      s *= a.scale * kLog2e;
+    }
+    const float mn = fmaxf(m, warp_max(s)), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m - base);
+    const float p = j0 + lane < count ? exp2f(s - base) : 0.f;
+    m = mn;
+    l = l * f + warp_add(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= f;
+    for (int j = 0; j < 32 && j0 + j < count; ++j) {
+      const float w = __shfl_sync(kAll, p, j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane + 32 * i < a.D) o[i] = fmaf(w, __bfloat162float(v[(j0 + j) * a.v_token + lane + 32 * i]), o[i]);
+    }
+    bool lost = true;                                      // every sum is NaN: it stays so
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lost = lost && (lane + 32 * i >= a.D || o[i] != o[i]);
+    if (__all_sync(kAll, lost) && l != l) break;
+  }
+  const bool some = !(l == 0.f);
+  __nv_bfloat16* to = a.out + q_at * a.out_token + h * a.out_head;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 32 * i < a.D) to[lane + 32 * i] = __float2bfloat16_rn(some ? o[i] / l : 0.f);
+  if (lane == 0 && a.lse)
+    a.lse[(long long)q_at * a.heads + h] = some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_prompt_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptTc a) {
+  using S = Shape<DP>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Ctl c;
+  const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t sq = base, ring = base + 2 * S::kTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // the block's sequence and rows: late (long) tiles of all heads come first
+  const int h = blockIdx.x % a.heads, slot = a.slots - 1 - (int)(blockIdx.x / a.heads);
+  int lo = 0, hi = a.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.starts_q[mid] / (2 * kRows) + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  auto clamp = [](int v, int x, int y) { return v < x ? x : v > y ? y : v; };
+  const int r0 = (slot - a.starts_q[lo] / (2 * kRows) - lo) * (2 * kRows);
+  const int q0 = clamp(a.starts_q[lo], 0, a.q_tokens), lq = clamp(a.starts_q[lo + 1], q0, a.q_tokens) - q0;
+  const int k0 = clamp(a.starts_k[lo], 0, a.k_tokens), lk = clamp(a.starts_k[lo + 1], k0, a.k_tokens) - k0;
+  if (r0 < 0 || r0 >= lq) return;
+  const int off = lk - lq;
+  Tile t[2];
+#pragma unroll
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    t[i].r0 = r0 + i * kRows;
+    const int end = (t[i].r0 + kRows < lq ? t[i].r0 + kRows : lq) + off;      // keys before `end` are seen
+    const int begin = a.window > 0 ? t[i].r0 + off - a.window + 1 : 0;
+    t[i].first = begin > 0 ? begin / kKeys : 0;
+    t[i].last = t[i].r0 < lq && end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    if (t[i].last <= t[i].first) t[i].first = t[i].last = 0;
+  }
+  const bool on0 = t[0].last > 0, on1 = t[1].last > 0;
+  const int j_first = on0 ? t[0].first : t[1].first, j_last = on1 ? t[1].last : t[0].last;
+
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&c.qfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.sfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.pfull[i]), 4);
+      tc::mbar_init(tc::smem_u32(&c.ofull[i]), 1);
+    }
+    for (int i = 0; i < S::kRing; ++i) {
+      tc::mbar_init(tc::smem_u32(&c.kvfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.kvempty[i]), 1);
+    }
+    tc::mbar_init(tc::smem_u32(&c.vgo), 1);
+    tc::mbar_init(tc::smem_u32(&c.vclean), 64);
+    c.stop = 0, c.bad_lo = 0x7fffffff, c.bad_hi = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&c.tmem), 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = c.tmem;
+  auto s_at = [&](int i) { return tmem + i * 128; };
+  auto o_at = [&](int i) { return tmem + 256 + i * 128; };
+  // whether a mask crosses step j of tile i, and of any tile at work on it
+  auto crossed = [&](int r, int j) {
+    return (j + 1) * kKeys - 1 > r + off || (a.window > 0 && j * kKeys <= r + kRows - 1 + off - a.window);
+  };
+  auto unclean = [&](int j) {
+    return (j >= t[0].first && j < t[0].last && crossed(t[0].r0, j)) ||
+           (j >= t[1].first && j < t[1].last && crossed(t[1].r0, j));
+  };
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kTmaWarp) {
+      if (lane == 0 && j_last > j_first) {
+        const int kh = h / a.group;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!(i ? on1 : on0)) continue;
+          const uint32_t bar = tc::smem_u32(&c.qfull[i]);
+          arrive_tx(bar, S::kTile);
+          for (int x = 0; x < DP / 64; ++x) tma_3d(sq + i * S::kTile + x * S::kBox, &mq, 64 * x, h, q0 + t[i].r0, bar);
+        }
+        // K(first), then V(j), K(j + 1)
+        const int loads = 2 * (j_last - j_first);
+        int u = 0;
+        for (; u < loads; ++u) {
+          const int slot_u = u % S::kRing, round = u / S::kRing;
+          if (round > 0 && !wait_for(c, c.kvempty[slot_u], (round - 1) & 1)) break;
+          const int j = j_first + u / 2;
+          const uint32_t bar = tc::smem_u32(&c.kvfull[slot_u]), dst = ring + slot_u * S::kTile;
+          const bool value = u & 1;
+          arrive_tx(bar, S::kTile);
+          for (int x = 0; x < DP / 64; ++x) tma_3d(dst + x * S::kBox, value ? &mv : &mk, 64 * x, kh, k0 + j * kKeys, bar);
+        }
+        if (u < loads)                               // a wait ran out: let the copies in flight land
+          for (int w = u > S::kRing ? u - S::kRing : 0; w < u; ++w)
+            tc::mbar_wait(tc::smem_u32(&c.kvfull[w % S::kRing]), (w / S::kRing) & 1, kLimitNs);
+      }
+    } else if (warp == kMmaWarp) {
+      constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
+      constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;      // B is N-major
+      bool ok = true;
+      auto ring_wait = [&](int u) { return warp_wait(c, c.kvfull[u % S::kRing], (u / S::kRing) & 1); };
+      auto scores = [&](int i, int u) {
+        if (lane == 0) {
+          const uint32_t kk = ring + u % S::kRing * S::kTile;
+#pragma unroll
+          for (int x = 0; x < DP / 16; ++x) {
+            const uint32_t o = (x / 4) * S::kBox + (x % 4) * 32;
+            tc::mma_bf16(s_at(i), desc_k(sq + i * S::kTile + o), desc_k(kk + o), id_s, x > 0);
+          }
+          tc::mma_commit(tc::smem_u32(&c.sfull[i]));
+        }
+        __syncwarp();
+      };
+      auto release = [&](int u) {
+        if (lane == 0) tc::mma_commit(tc::smem_u32(&c.kvempty[u % S::kRing]));
+        __syncwarp();
+      };
+      auto go_clean = [&]() {
+        if (lane == 0) arrive(tc::smem_u32(&c.vgo));
+        __syncwarp();
+      };
+      if (j_last > j_first) {
+        if (unclean(j_first)) go_clean();
+        ok = ring_wait(0);
+#pragma unroll
+        for (int i = 0; i < 2 && ok; ++i)
+          if ((i ? on1 : on0) && t[i].first == j_first) {
+            ok = warp_wait(c, c.qfull[i], 0);
+            if (ok) scores(i, 0);
+          }
+        if (ok) release(0);
+        unsigned np[2] = {0, 0}, nclean = 0;
+        for (int j = j_first; j < j_last && ok; ++j) {
+          const int uv = 2 * (j - j_first) + 1, uk = uv + 1;
+          ok = ring_wait(uv);
+          if (!ok) break;
+          if (unclean(j)) {
+            ok = warp_wait(c, c.vclean, nclean & 1);
+            ++nclean;
+            if (!ok) break;
+          }
+          if (j + 1 < j_last && unclean(j + 1)) go_clean();
+#pragma unroll
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (!(i ? on1 : on0)) continue;
+            if (j >= t[i].first && j < t[i].last) {
+              ok = warp_wait(c, c.pfull[i], np[i] & 1);
+              ++np[i];
+              if (!ok) break;
+              tc::fence_after_sync();
+              if (lane == 0) {
+                const uint32_t vv = ring + uv % S::kRing * S::kTile;
+#pragma unroll
+                for (int x = 0; x < kKeys / 16; ++x)
+                  tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, desc_n(vv + x * 2048), id_o, j > t[i].first || x > 0);
+                if (j == t[i].last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
+              }
+              __syncwarp();
+            }
+            if (j + 1 >= t[i].first && j + 1 < t[i].last) {
+              ok = ring_wait(uk) && warp_wait(c, c.qfull[i], 0);
+              if (ok) scores(i, uk);
+            }
+          }
+          if (!ok) break;
+          release(uv);
+          if (j + 1 < j_last) release(uk);
+        }
+      }
+    } else {
+      const int tid = threadIdx.x - 32 * kCleanWarp;           // 0 .. 63
+      unsigned ngo = 0;
+      for (int j = j_first; j < j_last; ++j) {
+        if (!unclean(j)) continue;
+        // the go for step j comes when the MMA warp is one step away: the slot's
+        // earlier load was consumed by then, so the parity below is of this one
+        const int uv = 2 * (j - j_first) + 1;
+        if (!warp_wait(c, c.vgo, ngo & 1) || !warp_wait(c, c.kvfull[uv % S::kRing], (uv / S::kRing) & 1)) break;
+        ++ngo;
+        const uint32_t vv = ring + uv % S::kRing * S::kTile;
+        const int valid = lk - j * kKeys;
+        for (int x = tid; x < S::kTile / 16; x += 64) {         // a 16-byte chunk: eight values of one key
+          const int key = (x >> 3) & 127;
+          const uint32_t at = vv + x * 16;
+          uint32_t u[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
+          bool odd = false;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if ((u[y] & 0x7f80u) == 0x7f80u) odd = true, u[y] &= 0xffff0000u;
+            if ((u[y] & 0x7f800000u) == 0x7f800000u) odd = true, u[y] &= 0x0000ffffu;
+            if (key >= valid) u[y] = 0;
+          }
+          if (odd || key >= valid)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+          if (odd && key < valid) {
+            atomicMin(&c.bad_lo, j * kKeys + key);
+            atomicMax(&c.bad_hi, j * kKeys + key);
+          }
+        }
+        tc::fence_async_smem();
+        arrive(tc::smem_u32(&c.vclean));
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2;
+    const Tile w = i ? t[1] : t[0];
+    const uint32_t quad = (uint32_t)(warp & 3) * 32u << 16;
+    const int row = w.r0 + (warp & 3) * 32 + lane;
+    const int at = row + off;                               // the last key this row sees
+    const float sc = a.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    unsigned ns = 0;
+    for (int j = w.first; j < w.last; ++j) {
+      ok = warp_wait(c, c.sfull[i], ns & 1);
+      ++ns;
+      if (!ok) break;
+      tc::fence_after_sync();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) ld32(s_at(i) + quad + 32 * x, s[x]);
+      ld_wait();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) tie(s[x]);
+      const int key = j * kKeys;
+      if (crossed(w.r0, j)) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            const int kj = key + 32 * x + y;
+            if (kj > at || (a.window > 0 && kj <= at - a.window)) s[x][y] = 0xff800000u;
+          }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 32; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[x][y]));
+      const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      const bool grow = mn > m + kSlack || (m == -INFINITY && mn > -INFINITY);
+      if (__any_sync(kAll, grow)) {
+        const float to = grow ? mn : m;
+        const float f = to == -INFINITY ? 1.f : ex2(m - to);
+        m = to;
+        l *= f;
+        if (j > w.first) {
+#pragma unroll 1
+          for (int x = 0; x < DP; x += 32) {
+            uint32_t o[32];
+            ld32(o_at(i) + quad + x, o);
+            ld_wait();
+            tie(o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            st32(o_at(i) + quad + x, o);
+          }
+        }
+      }
+      const float mb = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t p[32];
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          const uint32_t s0 = s[2 * x + y / 16][(2 * y) & 31], s1 = s[2 * x + y / 16][(2 * y + 1) & 31];
+          const float p0 = ex2(fmaf(__uint_as_float(s0), sc, -mb)), p1 = ex2(fmaf(__uint_as_float(s1), sc, -mb));
+          sum[(2 * y) & 3] += p0;
+          sum[(2 * y + 1) & 3] += p1;
+          p[y] = pack_bf16(p0, p1);
+        }
+        st32(s_at(i) + quad + 32 * x, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive(tc::smem_u32(&c.pfull[i]));
+    }
+    if (ok && w.last > 0) ok = warp_wait(c, c.ofull[i], 0);
+    tc::fence_after_sync();
+    const bool mine = row < lq;
+    const bool some = w.last > 0 && !(l == 0.f);
+    const float f = some ? 1.f / l : 0.f;
+    __nv_bfloat16* to = a.out + (long long)(q0 + row) * a.out_token + h * a.out_head;
+    const bool wide = ((size_t)to & 15) == 0;
+#pragma unroll 1
+    for (int x = 0; x < DP; x += 32) {
+      uint32_t o[32];
+      if (w.last > 0) {
+        ld32(o_at(i) + quad + x, o);
+        ld_wait();
+        tie(o);
+      }
+#pragma unroll
+      for (int y = 0; y < 32; ++y) {
+        const float v = !ok ? NAN : some ? __uint_as_float(o[y]) * f : 0.f;
+        o[y] = __float_as_uint(v);
+      }
+      if (mine) {
+#pragma unroll
+        for (int y = 0; y < 32; y += 8) {
+          if (x + y >= a.D) continue;
+          const uint4 v = make_uint4(pack_bf16(__uint_as_float(o[y]), __uint_as_float(o[y + 1])),
+                                     pack_bf16(__uint_as_float(o[y + 2]), __uint_as_float(o[y + 3])),
+                                     pack_bf16(__uint_as_float(o[y + 4]), __uint_as_float(o[y + 5])),
+                                     pack_bf16(__uint_as_float(o[y + 6]), __uint_as_float(o[y + 7])));
+          if (wide) {
+            *reinterpret_cast<uint4*>(to + x + y) = v;
+          } else {
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              reinterpret_cast<unsigned short*>(to)[x + y + z] = (unsigned short)(u[z / 2] >> (16 * (z & 1)));
+          }
+        }
+      }
+    }
+    if (mine && a.lse)
+      a.lse[(long long)(q0 + row) * a.heads + h] = !ok ? NAN : some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
+    // rows that see a value that was zeroed
+    const int from = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
+    unsigned again = __ballot_sync(kAll, mine && ok && c.bad_hi >= from && c.bad_lo <= at);
+    while (again) {
+      const int b = __ffs(again) - 1;
+      again &= again - 1;
+      const int rr = w.r0 + (warp & 3) * 32 + b, last = rr + off;
+      const int first = a.window > 0 && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
+      redo_row(a, h, q0 + rr, (long long)k0 + first, last - first + 1);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kMmaWarp) tc::tmem_free(tmem, 512);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static EncodeFn fn = nullptr;
+  static bool tried = false;
+  std::lock_guard<std::mutex> lock(launch_state_mutex());
+  if (!tried) {
+    tried = true;
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+    else
+      cudaGetLastError();
+  }
+  return fn;
+}
+
+// [tokens][heads][D] bf16, boxes of 128 tokens of one head and 64 columns
+bool encode(EncodeFn fn, CUtensorMap* m, const void* base, long long tokens, long long heads, int D, long long token,
+            long long head) {
+  // a distance that is never used may be anything: give the map a valid one
+  if (heads == 1) head = 64;
+  if (tokens == 1) token = head * heads;
+  if (token <= 0 || head <= 0 || token % 8 || head % 8 || ((size_t)base & 15)) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t stride[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2};
+  const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP>
+cudaError_t go(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptTc& p, cudaStream_t s) {
+  static bool set[kMaxDevices] = {};
+  {
+    std::lock_guard<std::mutex> lock(launch_state_mutex());
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(k_prompt_tc<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
+      if (e != cudaSuccess) return e;
+      set[dev] = true;
+    }
+  }
+  const long long grid = (long long)p.heads * p.slots;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  k_prompt_tc<DP><<<(unsigned)grid, kTcThreads, Shape<DP>::kSmem, s>>>(mq, mk, mv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// cudaErrorNotSupported: a type, size or alignment that the plain kernel takes
+cudaError_t launch_attn_prompt_tc(const moe_prompt_args& a, cudaStream_t s) {
+  if (a.dtype != MOE_BF16 || a.head_dim > 128 || a.k_tokens < 1 || !(a.scale > 0.f)) return cudaErrorNotSupported;
+  const EncodeFn fn = encoder();
+  CUtensorMap mq, mk, mv;
+  if (!fn || !encode(fn, &mq, a.q_d, a.q_tokens, a.heads, a.head_dim, a.q_token, a.q_head) ||
+      !encode(fn, &mk, a.k_d, a.k_tokens, a.kv_heads, a.head_dim, a.k_token, a.k_head) ||
+      !encode(fn, &mv, a.v_d, a.k_tokens, a.kv_heads, a.head_dim, a.v_token, a.v_head))
+    return cudaErrorNotSupported;
+  PromptTc p;
+  p.starts_q = a.starts_q_d, p.starts_k = a.starts_k_d;
+  p.q = (const __nv_bfloat16*)a.q_d, p.k = (const __nv_bfloat16*)a.k_d, p.v = (const __nv_bfloat16*)a.v_d;
+  p.out = (__nv_bfloat16*)a.out_d, p.lse = a.lse_d;
+  p.q_token = a.q_token, p.q_head = a.q_head, p.k_token = a.k_token, p.k_head = a.k_head;
+  p.v_token = a.v_token, p.v_head = a.v_head, p.out_token = a.out_token, p.out_head = a.out_head;
+  p.n = a.n, p.q_tokens = a.q_tokens, p.k_tokens = a.k_tokens;
+  p.heads = a.heads, p.group = a.heads / a.kv_heads, p.D = a.head_dim, p.window = a.window, p.scale = a.scale;
+  p.slots = a.q_tokens / (2 * kRows) + a.n;
+  return a.head_dim <= 64 ? go<64>(mq, mk, mv, p, s) : go<128>(mq, mk, mv, p, s);
+}
+
+}  // namespace moe
