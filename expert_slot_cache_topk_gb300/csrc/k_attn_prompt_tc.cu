@@ -299,78 +299,67 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::mbar_wait(tc::smem_u32(&c.kvfull[w % S::kRing]), (w / S::kRing) & 1, kLimitNs);
       }
     } else if (warp == kMmaWarp) {
-      constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
-      constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;      // B is N-major
-      bool ok = true;
-      auto ring_wait = [&](int u) { return warp_wait(c, c.kvfull[u % S::kRing], (u / S::kRing) & 1); };
-      auto scores = [&](int i, int u) {
-        if (lane == 0) {
-          const uint32_t kk = ring + u % S::kRing * S::kTile;
+      // One thread runs the whole loop: a wait on a finished phase then costs some
+      // 15 cycles, where a warp that votes on it pays over 100, and the loop's own
+      // time is what keeps the tensor cores waiting.
+      if (lane == 0 && j_last > j_first) {
+        constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
+        constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;      // B is N-major
+        const uint64_t dq[2] = {desc_k(sq), desc_k(sq + S::kTile)}, dk = desc_k(ring), dv = desc_n(ring);
+        auto ring_wait = [&](int u) { return wait_for(c, c.kvfull[u % S::kRing], (u / S::kRing) & 1); };
+        auto scores = [&](int i, int u) {
+          const uint64_t kk = dk + (u % S::kRing) * (S::kTile >> 4);
 #pragma unroll
           for (int x = 0; x < DP / 16; ++x) {
-            const uint32_t o = (x / 4) * S::kBox + (x % 4) * 32;
-            tc::mma_bf16(s_at(i), desc_k(sq + i * S::kTile + o), desc_k(kk + o), id_s, x > 0);
+            const uint32_t o = ((x / 4) * S::kBox + (x % 4) * 32) >> 4;
+            tc::mma_bf16(s_at(i), dq[i] + o, kk + o, id_s, x > 0);
           }
           tc::mma_commit(tc::smem_u32(&c.sfull[i]));
-        }
-        __syncwarp();
-      };
-      auto release = [&](int u) {
-        if (lane == 0) tc::mma_commit(tc::smem_u32(&c.kvempty[u % S::kRing]));
-        __syncwarp();
-      };
-      auto go_clean = [&]() {
-        if (lane == 0) arrive(tc::smem_u32(&c.vgo));
-        __syncwarp();
-      };
-      if (j_last > j_first) {
-        if (unclean(j_first)) go_clean();
-        ok = ring_wait(0);
+        };
+        auto release = [&](int u) { tc::mma_commit(tc::smem_u32(&c.kvempty[u % S::kRing])); };
+        if (unclean(j_first)) arrive(tc::smem_u32(&c.vgo));
+        bool ok = ring_wait(0);
 #pragma unroll
-        for (int i = 0; i < 2 && ok; ++i)
-          if ((i ? on1 : on0) && t[i].first == j_first) {
-            ok = warp_wait(c, c.qfull[i], 0);
-            if (ok) scores(i, 0);
+        for (int i = 0; i < 2; ++i)
+          if ((i ? on1 : on0) && ok) {
+            ok = wait_for(c, c.qfull[i], 0);
+            if (ok && t[i].first == j_first) scores(i, 0);
           }
         if (ok) release(0);
         unsigned np[2] = {0, 0}, nclean = 0;
         for (int j = j_first; j < j_last && ok; ++j) {
           const int uv = 2 * (j - j_first) + 1, uk = uv + 1;
-          ok = ring_wait(uv);
+          const bool more = j + 1 < j_last;
+          ok = ring_wait(uv) && (!more || ring_wait(uk));
           if (!ok) break;
           if (unclean(j)) {
-            ok = warp_wait(c, c.vclean, nclean & 1);
+            ok = wait_for(c, c.vclean, nclean & 1);
             ++nclean;
             if (!ok) break;
           }
-          if (j + 1 < j_last && unclean(j + 1)) go_clean();
+          if (more && unclean(j + 1)) arrive(tc::smem_u32(&c.vgo));
+          const uint64_t vv = dv + (uv % S::kRing) * (S::kTile >> 4);
 #pragma unroll
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (!(i ? on1 : on0)) continue;
-            if (j >= t[i].first && j < t[i].last) {
-              ok = warp_wait(c, c.pfull[i], np[i] & 1);
+          for (int i = 0; i < 2; ++i) {
+            if (j >= t[i].first && j < t[i].last && ok) {
+              ok = wait_for(c, c.pfull[i], np[i] & 1);
               ++np[i];
-              if (!ok) break;
-              tc::fence_after_sync();
-              if (lane == 0) {
-                const uint32_t vv = ring + uv % S::kRing * S::kTile;
+              if (ok) {
+                tc::fence_after_sync();
 #pragma unroll
                 for (int x = 0; x < kKeys / 16; ++x)
-                  tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, desc_n(vv + x * 2048), id_o, j > t[i].first || x > 0);
+                  tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, j > t[i].first || x > 0);
                 if (j == t[i].last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
               }
-              __syncwarp();
             }
-            if (j + 1 >= t[i].first && j + 1 < t[i].last) {
-              ok = ring_wait(uk) && warp_wait(c, c.qfull[i], 0);
-              if (ok) scores(i, uk);
-            }
+            if (ok && j + 1 >= t[i].first && j + 1 < t[i].last) scores(i, uk);
           }
           if (!ok) break;
           release(uv);
-          if (j + 1 < j_last) release(uk);
+          if (more) release(uk);
         }
       }
+      __syncwarp();
     } else {
       const int tid = threadIdx.x - 32 * kCleanWarp;           // 0 .. 63
       unsigned ngo = 0;
