@@ -67,7 +67,7 @@ struct PromptTc {
 };
 
 struct Ctl {
-  unsigned long long qfull[2], kvfull[8], kvempty[8], sfull[2], pfull[2], ofull[2], vgo, vclean;
+  unsigned long long qfull[2], kvfull[8], kvempty[8], sfull[2], pfull[2][2], ofull[2], vgo, vclean;
   uint32_t tmem;
   int stop;
   int bad_lo, bad_hi;            // keys (of the sequence) with a value that was zeroed: first, last
@@ -77,6 +77,31 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// two f32 at a time: a * b + c, and a + b
+__device__ __forceinline__ unsigned long long pair(float lo, float hi) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
 }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -150,6 +175,7 @@ __device__ __forceinline__ bool wait_for(Ctl& c, unsigned long long& bar, unsign
 
 // the whole warp waits and goes on, or stops, together
 __device__ __forceinline__ bool warp_wait(Ctl& c, unsigned long long& bar, unsigned parity) {
+  if (__all_sync(kAll, tc::mbar_try(tc::smem_u32(&bar), parity))) return true;
   return __all_sync(kAll, wait_for(c, bar, parity));
 }
 
@@ -242,7 +268,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&c.qfull[i]), 1);
       tc::mbar_init(tc::smem_u32(&c.sfull[i]), 1);
-      tc::mbar_init(tc::smem_u32(&c.pfull[i]), 4);
+      tc::mbar_init(tc::smem_u32(&c.pfull[i][0]), 4);
+      tc::mbar_init(tc::smem_u32(&c.pfull[i][1]), 4);
       tc::mbar_init(tc::smem_u32(&c.ofull[i]), 1);
     }
     for (int i = 0; i < S::kRing; ++i) {
@@ -342,15 +369,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (j >= t[i].first && j < t[i].last && ok) {
-              ok = wait_for(c, c.pfull[i], np[i] & 1);
-              ++np[i];
-              if (ok) {
+              // the weights come in two halves: the first 64 keys' product runs
+              // while the softmax works on the others
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                ok = ok && wait_for(c, c.pfull[i][z], np[i] & 1);
+                if (!ok) break;
                 tc::fence_after_sync();
 #pragma unroll
-                for (int x = 0; x < kKeys / 16; ++x)
+                for (int x = 4 * z; x < 4 * z + 4; ++x)
                   tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, j > t[i].first || x > 0);
-                if (j == t[i].last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
               }
+              ++np[i];
+              if (ok && j == t[i].last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
             }
             if (ok && j + 1 >= t[i].first && j + 1 < t[i].last) scores(i, uk);
           }
@@ -431,8 +462,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int y = 0; y < 32; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[x][y]));
-      const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        for (int y = 0; y < 32; y += 2)
+          mx[(y / 2) & 3] = max3(mx[(y / 2) & 3], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
+      const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
       const bool grow = mn > m + kSlack || (m == -INFINITY && mn > -INFINITY);
       if (__any_sync(kAll, grow)) {
         const float to = grow ? mn : m;
@@ -453,25 +485,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       const float mb = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const unsigned long long sc2 = pair(sc, sc), mb2 = pair(-mb, -mb);
+      unsigned long long sum[2] = {0ull, 0ull};                       // pairs of zeros
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         uint32_t p[32];
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
           const uint32_t s0 = s[2 * x + y / 16][(2 * y) & 31], s1 = s[2 * x + y / 16][(2 * y + 1) & 31];
-          const float p0 = ex2(fmaf(__uint_as_float(s0), sc, -mb)), p1 = ex2(fmaf(__uint_as_float(s1), sc, -mb));
-          sum[(2 * y) & 3] += p0;
-          sum[(2 * y + 1) & 3] += p1;
+          float p0, p1;
+          unpair(fma2(pair(__uint_as_float(s0), __uint_as_float(s1)), sc2, mb2), p0, p1);
+          p0 = ex2(p0), p1 = ex2(p1);
+          sum[y & 1] = add2(sum[y & 1], pair(p0, p1));
           p[y] = pack_bf16(p0, p1);
         }
         st32(s_at(i) + quad + 32 * x, p);
+        st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(tc::smem_u32(&c.pfull[i][x]));
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      st_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive(tc::smem_u32(&c.pfull[i]));
+      float a0, a1;
+      unpair(add2(sum[0], sum[1]), a0, a1);
+      l += a0 + a1;
     }
     if (ok && w.last > 0) ok = warp_wait(c, c.ofull[i], 0);
     tc::fence_after_sync();
