@@ -1,9 +1,17 @@
 // Attention over packed bf16 prompts on the tensor cores (head_dim up to 128).
 //
-// A block takes 256 queries of one head as two tiles of 128 rows.  Per tile and
-// 128 keys:  S = Q K^T (f32 in tensor memory);  one thread per row reads its
-// 128 scores, p = 2^(s scale log2e - m) with a running maximum m, and writes p
-// back as bf16 over the scores;  O += P V with P read from tensor memory.
+// A work item is two tiles of 128 rows of one key head.  A row is a query of one
+// of `pack` query heads that share the key head (pack divides the group), heads
+// varying fastest, so a tile holds 128 / pack tokens and grouped heads share
+// every key and value load, the mask's waste and short sequences' empty rows.
+// Per tile and 128 keys:  S = Q K^T (f32 in tensor memory);  one thread per row
+// reads its 128 scores, p = 2^(s scale log2e - m) with a running maximum m, and
+// writes p back as bf16 over the scores;  O += P V with P read from tensor memory.
+//
+// Blocks are persistent: a block that has finished loading an item cancels a
+// block of the grid that has not started yet (clusterlaunchcontrol) and takes its
+// item, so the next item's loads and first products run under this one's end,
+// and late tiles (the long ones under the causal mask) are handed out first.
 //
 // Warp roles (12 warps, one block per SM):
 //   warps 0-3, 4-7   softmax of tile 0 / tile 1: thread = row = tensor-memory lane;
@@ -63,15 +71,27 @@ struct PromptTc {
   float* lse;
   long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
   int n, q_tokens, k_tokens, heads, group, D, window, slots;
+  int pack, tile_tokens;         // query heads and tokens of a 128-row tile
   float scale;
 };
 
-struct Ctl {
-  unsigned long long qfull[2], kvfull[8], kvempty[8], sfull[2], pfull[2][2], ofull[2], vgo, vclean;
-  uint32_t tmem;
-  int stop;
+// One item, found by the load warp and read by all others
+struct Item {
+  int live;                      // 0: no more items
+  int q0, k0, lq, lk;            // the sequence's first query and key, and how many of each
+  int r0, head;                  // the first tile's first token; the first of its `pack` heads
   int bad_lo, bad_hi;            // keys (of the sequence) with a value that was zeroed: first, last
 };
+
+struct Ctl {
+  unsigned long long qfull[2], qempty[2], kvfull[8], kvempty[8], sfull[2], pfull[2][2], ofull[2], vgo, vclean;
+  unsigned long long ifull[2], iempty[2], next;
+  __align__(16) unsigned long long cancel[2];      // what clusterlaunchcontrol answered
+  Item item[2];
+  uint32_t tmem;
+  int stop;
+};
+constexpr int kItemReaders = 11;                   // the MMA thread, two cleaning warps, eight softmax warps
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -163,6 +183,10 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
 // false once a wait of the block has run out
 __device__ __forceinline__ bool wait_for(Ctl& c, unsigned long long& bar, unsigned parity) {
   const uint32_t b = tc::smem_u32(&bar);
@@ -183,6 +207,35 @@ __device__ __forceinline__ bool warp_wait(Ctl& c, unsigned long long& bar, unsig
 struct Tile {
   int r0, first, last;
 };
+struct Plan {
+  Tile t[2];
+  int off, first, last;          // key of query r: r + off; steps of the item
+};
+__device__ __forceinline__ Plan plan_of(const Item& it, int tile_tokens, int window) {
+  Plan p;
+  p.off = it.lk - it.lq;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    Tile& t = p.t[i];
+    t.r0 = it.r0 + i * tile_tokens;
+    const int end = (t.r0 + tile_tokens < it.lq ? t.r0 + tile_tokens : it.lq) + p.off;      // keys before `end` are seen
+    const int begin = window > 0 ? t.r0 + p.off - window + 1 : 0;
+    t.first = begin > 0 ? begin / kKeys : 0;
+    t.last = t.r0 < it.lq && end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    if (t.last <= t.first) t.first = t.last = 0;
+  }
+  p.first = p.t[0].last > 0 ? p.t[0].first : p.t[1].first;
+  p.last = p.t[1].last > 0 ? p.t[1].last : p.t[0].last;
+  return p;
+}
+// whether a mask crosses step j of a tile, and of any tile at work on the step
+__device__ __forceinline__ bool crossed(const Tile& t, int off, int tile_tokens, int window, int j) {
+  return (j + 1) * kKeys - 1 > t.r0 + off || (window > 0 && j * kKeys <= t.r0 + tile_tokens - 1 + off - window);
+}
+__device__ __forceinline__ bool unclean(const Plan& p, int tile_tokens, int window, int j) {
+  return (j >= p.t[0].first && j < p.t[0].last && crossed(p.t[0], p.off, tile_tokens, window, j)) ||
+         (j >= p.t[1].first && j < p.t[1].last && crossed(p.t[1], p.off, tile_tokens, window, j));
+}
 
 // One row again, by one warp: only the keys that the row sees are read
 __device__ __noinline__ void redo_row(const PromptTc& a, int h, int q_at, long long k_first, int count) {
@@ -234,43 +287,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t sq = base, ring = base + 2 * S::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // the block's sequence and rows: late (long) tiles of all heads come first
-  const int h = blockIdx.x % a.heads, slot = a.slots - 1 - (int)(blockIdx.x / a.heads);
-  int lo = 0, hi = a.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.starts_q[mid] / (2 * kRows) + mid <= slot) lo = mid;
-    else hi = mid;
-  }
-  auto clamp = [](int v, int x, int y) { return v < x ? x : v > y ? y : v; };
-  const int r0 = (slot - a.starts_q[lo] / (2 * kRows) - lo) * (2 * kRows);
-  const int q0 = clamp(a.starts_q[lo], 0, a.q_tokens), lq = clamp(a.starts_q[lo + 1], q0, a.q_tokens) - q0;
-  const int k0 = clamp(a.starts_k[lo], 0, a.k_tokens), lk = clamp(a.starts_k[lo + 1], k0, a.k_tokens) - k0;
-  if (r0 < 0 || r0 >= lq) return;
-  const int off = lk - lq;
-  Tile t[2];
-#pragma unroll
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    t[i].r0 = r0 + i * kRows;
-    const int end = (t[i].r0 + kRows < lq ? t[i].r0 + kRows : lq) + off;      // keys before `end` are seen
-    const int begin = a.window > 0 ? t[i].r0 + off - a.window + 1 : 0;
-    t[i].first = begin > 0 ? begin / kKeys : 0;
-    t[i].last = t[i].r0 < lq && end > 0 ? (end + kKeys - 1) / kKeys : 0;
-    if (t[i].last <= t[i].first) t[i].first = t[i].last = 0;
-  }
-  const bool on0 = t[0].last > 0, on1 = t[1].last > 0;
-  const int j_first = on0 ? t[0].first : t[1].first, j_last = on1 ? t[1].last : t[0].last;
+  const int tt = a.tile_tokens, window = a.window;
 
   if (threadIdx.x == 0) {
-#pragma unroll
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&c.qfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.qempty[i]), 1);
       tc::mbar_init(tc::smem_u32(&c.sfull[i]), 1);
       tc::mbar_init(tc::smem_u32(&c.pfull[i][0]), 4);
       tc::mbar_init(tc::smem_u32(&c.pfull[i][1]), 4);
       tc::mbar_init(tc::smem_u32(&c.ofull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.ifull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.iempty[i]), kItemReaders);
     }
     for (int i = 0; i < S::kRing; ++i) {
       tc::mbar_init(tc::smem_u32(&c.kvfull[i]), 1);
@@ -278,7 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc::mbar_init(tc::smem_u32(&c.vgo), 1);
     tc::mbar_init(tc::smem_u32(&c.vclean), 64);
-    c.stop = 0, c.bad_lo = 0x7fffffff, c.bad_hi = -1;
+    tc::mbar_init(tc::smem_u32(&c.next), 1);
+    c.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&c.tmem), 512);
@@ -288,53 +317,124 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = c.tmem;
   auto s_at = [&](int i) { return tmem + i * 128; };
   auto o_at = [&](int i) { return tmem + 256 + i * 128; };
-  // whether a mask crosses step j of tile i, and of any tile at work on it
-  auto crossed = [&](int r, int j) {
-    return (j + 1) * kKeys - 1 > r + off || (a.window > 0 && j * kKeys <= r + kRows - 1 + off - a.window);
-  };
-  auto unclean = [&](int j) {
-    return (j >= t[0].first && j < t[0].last && crossed(t[0].r0, j)) ||
-           (j >= t[1].first && j < t[1].last && crossed(t[1].r0, j));
-  };
 
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
-      if (lane == 0 && j_last > j_first) {
-        const int kh = h / a.group;
+      const int per_slot = a.heads / a.pack;
+      int unit = blockIdx.x;
+      unsigned published = 0, cancels = 0, nq[2] = {0, 0};
+      int u = 0;                                       // K / V loads so far
+      bool ok = true;
+      while (ok) {
+        Item it;
+        it.live = 1, it.bad_lo = 0x7fffffff, it.bad_hi = -1;
+        it.head = unit % per_slot * a.pack;
+        const int slot = a.slots - 1 - unit / per_slot;
+        int lo = 0, hi = a.n;                          // the last sequence whose tiles start at or before the slot
+        while (hi - lo > 1) {
+          const int step = (hi - lo + 31) / 32, x = lo + lane * step;
+          const bool below = lane == 0 || (x < hi && a.starts_q[x] / (2 * tt) + x <= slot);
+          const int m = 31 - __clz(__ballot_sync(kAll, below));
+          lo += m * step;
+          hi = lo + step < hi ? lo + step : hi;
+        }
+        auto clamp = [](int v, int x, int y) { return v < x ? x : v > y ? y : v; };
+        const int s0 = a.starts_q[lo];
+        it.r0 = (slot - s0 / (2 * tt) - lo) * (2 * tt);
+        it.q0 = clamp(s0, 0, a.q_tokens), it.lq = clamp(a.starts_q[lo + 1], it.q0, a.q_tokens) - it.q0;
+        it.k0 = clamp(a.starts_k[lo], 0, a.k_tokens), it.lk = clamp(a.starts_k[lo + 1], it.k0, a.k_tokens) - it.k0;
+        if (it.r0 >= 0 && it.r0 < it.lq) {
+          const int z = published & 1;
+          if (published >= 2) ok = warp_wait(c, c.iempty[z], (published / 2 - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            c.item[z] = it;
+            arrive(tc::smem_u32(&c.ifull[z]));
+          }
+          ++published;
+          const Plan p = plan_of(it, tt, window);
+          if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!(i ? on1 : on0)) continue;
-          const uint32_t bar = tc::smem_u32(&c.qfull[i]);
-          arrive_tx(bar, S::kTile);
-          for (int x = 0; x < DP / 64; ++x) tma_3d(sq + i * S::kTile + x * S::kBox, &mq, 64 * x, h, q0 + t[i].r0, bar);
+            for (int i = 0; i < 2; ++i) {
+              if (p.t[i].last == 0 || !ok) continue;
+              if (nq[i] > 0) ok = wait_for(c, c.qempty[i], (nq[i] - 1) & 1);
+              ++nq[i];
+              if (!ok) continue;
+              const uint32_t bar = tc::smem_u32(&c.qfull[i]);
+              arrive_tx(bar, tt * a.pack * DP * 2);
+              for (int x = 0; x < DP / 64; ++x)
+                tma_3d(sq + i * S::kTile + x * S::kBox, &mq, 64 * x, it.head, it.q0 + p.t[i].r0, bar);
+            }
+            const int kh = it.head / a.group;
+            for (int w = 0; w < 2 * (p.last - p.first) && ok; ++w) {        // K(first), then V(j), K(j + 1)
+              const int z = u % S::kRing, round = u / S::kRing;
+              if (round > 0) ok = wait_for(c, c.kvempty[z], (round - 1) & 1);
+              if (!ok) break;
+              const uint32_t bar = tc::smem_u32(&c.kvfull[z]), dst = ring + z * S::kTile;
+              arrive_tx(bar, S::kTile);
+              for (int x = 0; x < DP / 64; ++x)
+                tma_3d(dst + x * S::kBox, w & 1 ? &mv : &mk, 64 * x, kh, it.k0 + (p.first + w / 2) * kKeys, bar);
+              ++u;
+            }
+          }
+          ok = __shfl_sync(kAll, ok, 0);
         }
-        // K(first), then V(j), K(j + 1)
-        const int loads = 2 * (j_last - j_first);
-        int u = 0;
-        for (; u < loads; ++u) {
-          const int slot_u = u % S::kRing, round = u / S::kRing;
-          if (round > 0 && !wait_for(c, c.kvempty[slot_u], (round - 1) & 1)) break;
-          const int j = j_first + u / 2;
-          const uint32_t bar = tc::smem_u32(&c.kvfull[slot_u]), dst = ring + slot_u * S::kTile;
-          const bool value = u & 1;
-          arrive_tx(bar, S::kTile);
-          for (int x = 0; x < DP / 64; ++x) tma_3d(dst + x * S::kBox, value ? &mv : &mk, 64 * x, kh, k0 + j * kKeys, bar);
+        if (!ok) break;
+        // ask for the next unit once this one's loads are out (earlier, and a block would
+        // hold long units that an idle one could take)
+        if (lane == 0) {
+          tc::fence_async_smem();
+          arrive_tx(tc::smem_u32(&c.next), 16);
+          asm volatile(
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                  tc::smem_u32(c.cancel)),
+              "r"(tc::smem_u32(&c.next))
+              : "memory");
         }
-        if (u < loads)                               // a wait ran out: let the copies in flight land
-          for (int w = u > S::kRing ? u - S::kRing : 0; w < u; ++w)
-            tc::mbar_wait(tc::smem_u32(&c.kvfull[w % S::kRing]), (w / S::kRing) & 1, kLimitNs);
+        ++cancels;
+        ok = warp_wait(c, c.next, (cancels - 1) & 1);
+        if (!ok) break;
+        unsigned took, bx;
+        asm volatile(
+            "{ .reg .pred p; .reg .b128 h; .reg .b32 y, z, w;\n"
+            "ld.shared.b128 h, [%2];\n"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+            "selp.u32 %0, 1, 0, p;\n"
+            "mov.u32 %1, 0;\n"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h; }"
+            : "=r"(took), "=r"(bx)
+            : "r"(tc::smem_u32(c.cancel))
+            : "memory");
+        if (!took) break;
+        unit = (int)bx;
+        __syncwarp();
+      }
+      if (ok) {                                        // tell the others that there is no more
+        const int z = published & 1;
+        if (published >= 2) ok = warp_wait(c, c.iempty[z], (published / 2 - 1) & 1);
+        if (ok && lane == 0) {
+          c.item[z].live = 0;
+          arrive(tc::smem_u32(&c.ifull[z]));
+        }
+      }
+      if (!ok && lane == 0) {                          // a wait ran out: let what is in flight land
+        if (cancels > 0) tc::mbar_wait(tc::smem_u32(&c.next), (cancels - 1) & 1, kLimitNs / 8);
+        for (int w = u > S::kRing ? u - S::kRing : 0; w < u; ++w)
+          tc::mbar_wait(tc::smem_u32(&c.kvfull[w % S::kRing]), (w / S::kRing) & 1, kLimitNs / 8);
+        for (int i = 0; i < 2; ++i)
+          if (nq[i] > 0) tc::mbar_wait(tc::smem_u32(&c.qfull[i]), (nq[i] - 1) & 1, kLimitNs / 8);
       }
     } else if (warp == kMmaWarp) {
       // One thread runs the whole loop: a wait on a finished phase then costs some
       // 15 cycles, where a warp that votes on it pays over 100, and the loop's own
       // time is what keeps the tensor cores waiting.
-      if (lane == 0 && j_last > j_first) {
+      if (lane == 0) {
         constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
         constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;      // B is N-major
         const uint64_t dq[2] = {desc_k(sq), desc_k(sq + S::kTile)}, dk = desc_k(ring), dv = desc_n(ring);
         auto ring_wait = [&](int u) { return wait_for(c, c.kvfull[u % S::kRing], (u / S::kRing) & 1); };
-        auto scores = [&](int i, int u) {
+        auto scores = [&](int i, int u, bool last) {
           const uint64_t kk = dk + (u % S::kRing) * (S::kTile >> 4);
 #pragma unroll
           for (int x = 0; x < DP / 16; ++x) {
@@ -342,223 +442,287 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::mma_bf16(s_at(i), dq[i] + o, kk + o, id_s, x > 0);
           }
           tc::mma_commit(tc::smem_u32(&c.sfull[i]));
+          if (last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
         };
         auto release = [&](int u) { tc::mma_commit(tc::smem_u32(&c.kvempty[u % S::kRing])); };
-        if (unclean(j_first)) arrive(tc::smem_u32(&c.vgo));
-        bool ok = ring_wait(0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if ((i ? on1 : on0) && ok) {
-            ok = wait_for(c, c.qfull[i], 0);
-            if (ok && t[i].first == j_first) scores(i, 0);
-          }
-        if (ok) release(0);
-        unsigned np[2] = {0, 0}, nclean = 0;
-        for (int j = j_first; j < j_last && ok; ++j) {
-          const int uv = 2 * (j - j_first) + 1, uk = uv + 1;
-          const bool more = j + 1 < j_last;
-          ok = ring_wait(uv) && (!more || ring_wait(uk));
+        unsigned np[2] = {0, 0}, nq[2] = {0, 0}, nclean = 0;
+        int u0 = 0;                                    // the item's first K / V load
+        bool ok = true;
+        for (unsigned n = 0; ok; ++n) {
+          ok = wait_for(c, c.ifull[n & 1], (n / 2) & 1);
           if (!ok) break;
-          if (unclean(j)) {
-            ok = wait_for(c, c.vclean, nclean & 1);
-            ++nclean;
-            if (!ok) break;
-          }
-          if (more && unclean(j + 1)) arrive(tc::smem_u32(&c.vgo));
-          const uint64_t vv = dv + (uv % S::kRing) * (S::kTile >> 4);
+          const Item it = c.item[n & 1];
+          arrive(tc::smem_u32(&c.iempty[n & 1]));
+          if (!it.live) break;
+          const Plan p = plan_of(it, tt, window);
+          if (p.last <= p.first) continue;
+          if (unclean(p, tt, window, p.first)) arrive(tc::smem_u32(&c.vgo));
+          ok = ring_wait(u0);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (j >= t[i].first && j < t[i].last && ok) {
-              // the weights come in two halves: the first 64 keys' product runs
-              // while the softmax works on the others
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                ok = ok && wait_for(c, c.pfull[i][z], np[i] & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-#pragma unroll
-                for (int x = 4 * z; x < 4 * z + 4; ++x)
-                  tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, j > t[i].first || x > 0);
-              }
-              ++np[i];
-              if (ok && j == t[i].last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
+          for (int i = 0; i < 2; ++i)
+            if (p.t[i].last > 0 && ok) {
+              ok = wait_for(c, c.qfull[i], nq[i] & 1);
+              ++nq[i];
+              if (ok && p.t[i].first == p.first) scores(i, u0, p.t[i].last == p.first + 1);
             }
-            if (ok && j + 1 >= t[i].first && j + 1 < t[i].last) scores(i, uk);
+          if (ok) release(u0);
+          for (int j = p.first; j < p.last && ok; ++j) {
+            const int uv = u0 + 2 * (j - p.first) + 1, uk = uv + 1;
+            const bool more = j + 1 < p.last;
+            ok = ring_wait(uv) && (!more || ring_wait(uk));
+            if (!ok) break;
+            if (unclean(p, tt, window, j)) {
+              ok = wait_for(c, c.vclean, nclean & 1);
+              ++nclean;
+              if (!ok) break;
+            }
+            if (more && unclean(p, tt, window, j + 1)) arrive(tc::smem_u32(&c.vgo));
+            const uint64_t vv = dv + (uv % S::kRing) * (S::kTile >> 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const Tile& t = p.t[i];
+              if (j >= t.first && j < t.last && ok) {
+                // the weights come in two halves: the first 64 keys' product runs
+                // while the softmax works on the others
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  ok = ok && wait_for(c, c.pfull[i][z], np[i] & 1);
+                  if (!ok) break;
+                  tc::fence_after_sync();
+#pragma unroll
+                  for (int x = 4 * z; x < 4 * z + 4; ++x)
+                    tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, j > t.first || x > 0);
+                }
+                ++np[i];
+                if (ok && j == t.last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
+              }
+              if (ok && j + 1 >= t.first && j + 1 < t.last) scores(i, uk, j + 2 == t.last);
+            }
+            if (!ok) break;
+            release(uv);
+            if (more) release(uk);
           }
-          if (!ok) break;
-          release(uv);
-          if (more) release(uk);
+          u0 += 2 * (p.last - p.first);
         }
       }
       __syncwarp();
     } else {
       const int tid = threadIdx.x - 32 * kCleanWarp;           // 0 .. 63
       unsigned ngo = 0;
-      for (int j = j_first; j < j_last; ++j) {
-        if (!unclean(j)) continue;
-        // the go for step j comes when the MMA warp is one step away: the slot's
-        // earlier load was consumed by then, so the parity below is of this one
-        const int uv = 2 * (j - j_first) + 1;
-        if (!warp_wait(c, c.vgo, ngo & 1) || !warp_wait(c, c.kvfull[uv % S::kRing], (uv / S::kRing) & 1)) break;
-        ++ngo;
-        const uint32_t vv = ring + uv % S::kRing * S::kTile;
-        const int valid = lk - j * kKeys;
-        for (int x = tid; x < S::kTile / 16; x += 64) {         // a 16-byte chunk: eight values of one key
-          const int key = (x >> 3) & 127;
-          const uint32_t at = vv + x * 16;
-          uint32_t u[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
-          bool odd = false;
+      int u0 = 0;
+      for (unsigned n = 0;; ++n) {
+        if (!warp_wait(c, c.ifull[n & 1], (n / 2) & 1)) break;
+        Item& it = c.item[n & 1];
+        if (!it.live) break;
+        const Plan p = plan_of(it, tt, window);
+        const int lk = it.lk;
+        bool ok = true;
+        for (int j = p.first; j < p.last; ++j) {
+          if (!unclean(p, tt, window, j)) continue;
+          // the go for step j comes when the MMA thread is one step away: the slot's
+          // earlier load was consumed by then, so the parity below is of this one
+          const int uv = u0 + 2 * (j - p.first) + 1;
+          ok = warp_wait(c, c.vgo, ngo & 1) && warp_wait(c, c.kvfull[uv % S::kRing], (uv / S::kRing) & 1);
+          if (!ok) break;
+          ++ngo;
+          const uint32_t vv = ring + uv % S::kRing * S::kTile;
+          const int valid = lk - j * kKeys;
+          // 0 * x summed up is NaN once an x is not finite: first look, then mend
+          __nv_bfloat162 look[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if ((u[y] & 0x7f80u) == 0x7f80u) odd = true, u[y] &= 0xffff0000u;
-            if ((u[y] & 0x7f800000u) == 0x7f800000u) odd = true, u[y] &= 0x0000ffffu;
-            if (key >= valid) u[y] = 0;
+          for (int y = 0; y < 4; ++y) look[y] = __floats2bfloat162_rn(0.f, 0.f);
+          const __nv_bfloat162 zero = look[0];
+#pragma unroll 8
+          for (int x = tid; x < S::kTile / 16; x += 64) {         // a 16-byte chunk: eight values of one key
+            uint32_t v[4];
+            lds128(vv + x * 16, v);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) look[y] = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v[y]), zero, look[y]);
           }
-          if (odd || key >= valid)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
-          if (odd && key < valid) {
-            atomicMin(&c.bad_lo, j * kKeys + key);
-            atomicMax(&c.bad_hi, j * kKeys + key);
-          }
+          look[0] = __hadd2(__hadd2(look[0], look[1]), __hadd2(look[2], look[3]));
+          const float seen = __low2float(look[0]) + __high2float(look[0]);
+          if (seen != 0.f || valid < kKeys)
+            for (int x = tid; x < S::kTile / 16; x += 64) {
+              const int key = (x >> 3) & 127;
+              uint32_t v[4];
+              lds128(vv + x * 16, v);
+              bool odd = false;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if ((v[y] & 0x7f80u) == 0x7f80u) odd = true, v[y] &= 0xffff0000u;
+                if ((v[y] & 0x7f800000u) == 0x7f800000u) odd = true, v[y] &= 0x0000ffffu;
+                if (key >= valid) v[y] = 0;
+              }
+              if (odd || key >= valid)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(vv + x * 16), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                             : "memory");
+              if (odd && key < valid) {
+                atomicMin(&it.bad_lo, j * kKeys + key);
+                atomicMax(&it.bad_hi, j * kKeys + key);
+              }
+            }
+          tc::fence_async_smem();
+          arrive(tc::smem_u32(&c.vclean));
         }
-        tc::fence_async_smem();
-        arrive(tc::smem_u32(&c.vclean));
+        if (!ok) break;
+        u0 += 2 * (p.last - p.first);
+        __syncwarp();
+        if (lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2;
-    const Tile w = i ? t[1] : t[0];
     const uint32_t quad = (uint32_t)(warp & 3) * 32u << 16;
-    const int row = w.r0 + (warp & 3) * 32 + lane;
-    const int at = row + off;                               // the last key this row sees
+    const int in_tile = (warp & 3) * 32 + lane;             // the thread's row of the tile
+    const int row_token = in_tile / a.pack, row_head = in_tile - row_token * a.pack;
     const float sc = a.scale * kLog2e;
-    float m = -INFINITY, l = 0.f;
+    const unsigned long long sc2 = pair(sc, sc);
+    unsigned ns = 0, no = 0;
     bool ok = true;
-    unsigned ns = 0;
-    for (int j = w.first; j < w.last; ++j) {
-      ok = warp_wait(c, c.sfull[i], ns & 1);
-      ++ns;
+    for (unsigned n = 0; ok; ++n) {
+      ok = warp_wait(c, c.ifull[n & 1], (n / 2) & 1);
       if (!ok) break;
-      tc::fence_after_sync();
-      uint32_t s[4][32];
+      const Item& it = c.item[n & 1];
+      if (!it.live) break;
+      const int q0 = it.q0, k0 = it.k0, lq = it.lq;
+      const Plan p = plan_of(it, tt, window);
+      const Tile w = i ? p.t[1] : p.t[0];
+      const int row = w.r0 + row_token, head = it.head + row_head;
+      const int at = row + p.off;                           // the last key this row sees
+      float m = -INFINITY, l = 0.f;
+      for (int j = w.first; j < w.last; ++j) {
+        ok = warp_wait(c, c.sfull[i], ns & 1);
+        ++ns;
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t s[4][32];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ld32(s_at(i) + quad + 32 * x, s[x]);
-      ld_wait();
+        for (int x = 0; x < 4; ++x) ld32(s_at(i) + quad + 32 * x, s[x]);
+        ld_wait();
 #pragma unroll
-      for (int x = 0; x < 4; ++x) tie(s[x]);
-      const int key = j * kKeys;
-      if (crossed(w.r0, j)) {
+        for (int x = 0; x < 4; ++x) tie(s[x]);
+        const int key = j * kKeys;
+        if (crossed(w, p.off, tt, window, j)) {
+          const int hi = at - key, lo = window > 0 ? hi - window : -1;   // seen: lo < position <= hi
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (32 * x + y > hi) s[x][y] = 0xff800000u;
+          if (lo >= 0) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (32 * x + y <= lo) s[x][y] = 0xff800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
+          for (int y = 0; y < 32; y += 2)
+            mx[(y / 2) & 3] = max3(mx[(y / 2) & 3], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
+        const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+        const bool grow = mn > m + kSlack || (m == -INFINITY && mn > -INFINITY);
+        if (__any_sync(kAll, grow)) {
+          const float to = grow ? mn : m;
+          const float f = to == -INFINITY ? 1.f : ex2(m - to);
+          m = to;
+          l *= f;
+          if (j > w.first) {
+#pragma unroll 1
+            for (int x = 0; x < DP; x += 32) {
+              uint32_t o[32];
+              ld32(o_at(i) + quad + x, o);
+              ld_wait();
+              tie(o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              st32(o_at(i) + quad + x, o);
+            }
+          }
+        }
+        const float mb = m == -INFINITY ? 0.f : m;
+        const unsigned long long mb2 = pair(-mb, -mb);
+        unsigned long long sum[2] = {0ull, 0ull};                       // pairs of zeros
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t pw[32];
+#pragma unroll
           for (int y = 0; y < 32; ++y) {
-            const int kj = key + 32 * x + y;
-            if (kj > at || (a.window > 0 && kj <= at - a.window)) s[x][y] = 0xff800000u;
+            const uint32_t s0 = s[2 * x + y / 16][(2 * y) & 31], s1 = s[2 * x + y / 16][(2 * y + 1) & 31];
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(s0), __uint_as_float(s1)), sc2, mb2), p0, p1);
+            p0 = ex2(p0), p1 = ex2(p1);
+            sum[y & 1] = add2(sum[y & 1], pair(p0, p1));
+            pw[y] = pack_bf16(p0, p1);
           }
+          st32(s_at(i) + quad + 32 * x, pw);
+          st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive(tc::smem_u32(&c.pfull[i][x]));
+        }
+        float a0, a1;
+        unpair(add2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 32; y += 2)
-          mx[(y / 2) & 3] = max3(mx[(y / 2) & 3], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
-      const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
-      const bool grow = mn > m + kSlack || (m == -INFINITY && mn > -INFINITY);
-      if (__any_sync(kAll, grow)) {
-        const float to = grow ? mn : m;
-        const float f = to == -INFINITY ? 1.f : ex2(m - to);
-        m = to;
-        l *= f;
-        if (j > w.first) {
+      if (ok && w.last > 0) {
+        ok = warp_wait(c, c.ofull[i], no & 1);
+        ++no;
+      }
+      tc::fence_after_sync();
+      const bool mine = row < lq && row_token < tt;
+      const bool some = w.last > 0 && !(l == 0.f);
+      const float f = some ? 1.f / l : 0.f;
+      __nv_bfloat16* to = a.out + (long long)(q0 + row) * a.out_token + head * a.out_head;
+      const bool wide = ((size_t)to & 15) == 0;
 #pragma unroll 1
-          for (int x = 0; x < DP; x += 32) {
-            uint32_t o[32];
-            ld32(o_at(i) + quad + x, o);
-            ld_wait();
-            tie(o);
+      for (int x = 0; x < DP; x += 32) {
+        uint32_t o[32];
+        if (w.last > 0) {
+          ld32(o_at(i) + quad + x, o);
+          ld_wait();
+          tie(o);
+        }
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-            st32(o_at(i) + quad + x, o);
+        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(!ok ? NAN : some ? __uint_as_float(o[y]) * f : 0.f);
+        if (mine) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 8) {
+            if (x + y >= a.D) continue;
+            const uint4 v = make_uint4(pack_bf16(__uint_as_float(o[y]), __uint_as_float(o[y + 1])),
+                                       pack_bf16(__uint_as_float(o[y + 2]), __uint_as_float(o[y + 3])),
+                                       pack_bf16(__uint_as_float(o[y + 4]), __uint_as_float(o[y + 5])),
+                                       pack_bf16(__uint_as_float(o[y + 6]), __uint_as_float(o[y + 7])));
+            if (wide) {
+              *reinterpret_cast<uint4*>(to + x + y) = v;
+            } else {
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int z = 0; z < 8; ++z)
+                reinterpret_cast<unsigned short*>(to)[x + y + z] = (unsigned short)(u[z / 2] >> (16 * (z & 1)));
+            }
           }
         }
       }
-      const float mb = m == -INFINITY ? 0.f : m;
-      const unsigned long long sc2 = pair(sc, sc), mb2 = pair(-mb, -mb);
-      unsigned long long sum[2] = {0ull, 0ull};                       // pairs of zeros
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t p[32];
-#pragma unroll
-        for (int y = 0; y < 32; ++y) {
-          const uint32_t s0 = s[2 * x + y / 16][(2 * y) & 31], s1 = s[2 * x + y / 16][(2 * y + 1) & 31];
-          float p0, p1;
-          unpair(fma2(pair(__uint_as_float(s0), __uint_as_float(s1)), sc2, mb2), p0, p1);
-          p0 = ex2(p0), p1 = ex2(p1);
-          sum[y & 1] = add2(sum[y & 1], pair(p0, p1));
-          p[y] = pack_bf16(p0, p1);
-        }
-        st32(s_at(i) + quad + 32 * x, p);
-        st_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) arrive(tc::smem_u32(&c.pfull[i][x]));
+      tc::fence_before_sync();
+      if (mine && a.lse)
+        a.lse[(long long)(q0 + row) * a.heads + head] = !ok ? NAN : some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
+      // rows that see a value that was zeroed
+      const int from = window > 0 && at - window + 1 > 0 ? at - window + 1 : 0;
+      unsigned again = __ballot_sync(kAll, mine && ok && it.bad_hi >= from && it.bad_lo <= at);
+      while (again) {
+        const int b = __ffs(again) - 1;
+        again &= again - 1;
+        const int rr = __shfl_sync(kAll, row, b), hh = __shfl_sync(kAll, head, b), last = rr + p.off;
+        const int first = window > 0 && last - window + 1 > 0 ? last - window + 1 : 0;
+        redo_row(a, hh, q0 + rr, (long long)k0 + first, last - first + 1);
       }
-      float a0, a1;
-      unpair(add2(sum[0], sum[1]), a0, a1);
-      l += a0 + a1;
-    }
-    if (ok && w.last > 0) ok = warp_wait(c, c.ofull[i], 0);
-    tc::fence_after_sync();
-    const bool mine = row < lq;
-    const bool some = w.last > 0 && !(l == 0.f);
-    const float f = some ? 1.f / l : 0.f;
-    __nv_bfloat16* to = a.out + (long long)(q0 + row) * a.out_token + h * a.out_head;
-    const bool wide = ((size_t)to & 15) == 0;
-#pragma unroll 1
-    for (int x = 0; x < DP; x += 32) {
-      uint32_t o[32];
-      if (w.last > 0) {
-        ld32(o_at(i) + quad + x, o);
-        ld_wait();
-        tie(o);
-      }
-#pragma unroll
-      for (int y = 0; y < 32; ++y) {
-        const float v = !ok ? NAN : some ? __uint_as_float(o[y]) * f : 0.f;
-        o[y] = __float_as_uint(v);
-      }
-      if (mine) {
-#pragma unroll
-        for (int y = 0; y < 32; y += 8) {
-          if (x + y >= a.D) continue;
-          const uint4 v = make_uint4(pack_bf16(__uint_as_float(o[y]), __uint_as_float(o[y + 1])),
-                                     pack_bf16(__uint_as_float(o[y + 2]), __uint_as_float(o[y + 3])),
-                                     pack_bf16(__uint_as_float(o[y + 4]), __uint_as_float(o[y + 5])),
-                                     pack_bf16(__uint_as_float(o[y + 6]), __uint_as_float(o[y + 7])));
-          if (wide) {
-            *reinterpret_cast<uint4*>(to + x + y) = v;
-          } else {
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-              reinterpret_cast<unsigned short*>(to)[x + y + z] = (unsigned short)(u[z / 2] >> (16 * (z & 1)));
-          }
-        }
-      }
-    }
-    if (mine && a.lse)
-      a.lse[(long long)(q0 + row) * a.heads + h] = !ok ? NAN : some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
-    // rows that see a value that was zeroed
-    const int from = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
-    unsigned again = __ballot_sync(kAll, mine && ok && c.bad_hi >= from && c.bad_lo <= at);
-    while (again) {
-      const int b = __ffs(again) - 1;
-      again &= again - 1;
-      const int rr = w.r0 + (warp & 3) * 32 + b, last = rr + off;
-      const int first = a.window > 0 && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
-      redo_row(a, h, q0 + rr, (long long)k0 + first, last - first + 1);
+      __syncwarp();
+      if (lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
     }
   }
   tc::fence_before_sync();
@@ -588,16 +752,16 @@ EncodeFn encoder() {
   return fn;
 }
 
-// [tokens][heads][D] bf16, boxes of 128 tokens of one head and 64 columns
+// [tokens][heads][D] bf16, boxes of 64 columns, `box_heads` heads and `box_tokens` tokens
 bool encode(EncodeFn fn, CUtensorMap* m, const void* base, long long tokens, long long heads, int D, long long token,
-            long long head) {
+            long long head, int box_heads, int box_tokens) {
   // a distance that is never used may be anything: give the map a valid one
   if (heads == 1) head = 64;
   if (tokens == 1) token = head * heads;
   if (token <= 0 || head <= 0 || token % 8 || head % 8 || ((size_t)base & 15)) return false;
   const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t stride[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2};
-  const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -617,7 +781,7 @@ cudaError_t go(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
       set[dev] = true;
     }
   }
-  const long long grid = (long long)p.heads * p.slots;
+  const long long grid = (long long)(p.heads / p.pack) * p.slots;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   k_prompt_tc<DP><<<(unsigned)grid, kTcThreads, Shape<DP>::kSmem, s>>>(mq, mk, mv, p);
   return cudaGetLastError();
@@ -630,19 +794,26 @@ cudaError_t launch_attn_prompt_tc(const moe_prompt_args& a, cudaStream_t s) {
   if (a.dtype != MOE_BF16 || a.head_dim > 128 || a.k_tokens < 1 || !(a.scale > 0.f)) return cudaErrorNotSupported;
   const EncodeFn fn = encoder();
   CUtensorMap mq, mk, mv;
-  if (!fn || !encode(fn, &mq, a.q_d, a.q_tokens, a.heads, a.head_dim, a.q_token, a.q_head) ||
-      !encode(fn, &mk, a.k_d, a.k_tokens, a.kv_heads, a.head_dim, a.k_token, a.k_head) ||
-      !encode(fn, &mv, a.v_d, a.k_tokens, a.kv_heads, a.head_dim, a.v_token, a.v_head))
-    return cudaErrorNotSupported;
   PromptTc p;
+  // heads of a tile: the divisor of the group that fills most of its 128 rows,
+  // the largest of those (more heads share the loads)
+  p.group = a.heads / a.kv_heads;
+  p.pack = 1;
+  for (int d = 2; d <= p.group; ++d)
+    if (p.group % d == 0 && kRows / d * d >= kRows / p.pack * p.pack) p.pack = d;
+  p.tile_tokens = kRows / p.pack;
+  if (!fn || !encode(fn, &mq, a.q_d, a.q_tokens, a.heads, a.head_dim, a.q_token, a.q_head, p.pack, p.tile_tokens) ||
+      !encode(fn, &mk, a.k_d, a.k_tokens, a.kv_heads, a.head_dim, a.k_token, a.k_head, 1, kKeys) ||
+      !encode(fn, &mv, a.v_d, a.k_tokens, a.kv_heads, a.head_dim, a.v_token, a.v_head, 1, kKeys))
+    return cudaErrorNotSupported;
   p.starts_q = a.starts_q_d, p.starts_k = a.starts_k_d;
   p.q = (const __nv_bfloat16*)a.q_d, p.k = (const __nv_bfloat16*)a.k_d, p.v = (const __nv_bfloat16*)a.v_d;
   p.out = (__nv_bfloat16*)a.out_d, p.lse = a.lse_d;
   p.q_token = a.q_token, p.q_head = a.q_head, p.k_token = a.k_token, p.k_head = a.k_head;
   p.v_token = a.v_token, p.v_head = a.v_head, p.out_token = a.out_token, p.out_head = a.out_head;
   p.n = a.n, p.q_tokens = a.q_tokens, p.k_tokens = a.k_tokens;
-  p.heads = a.heads, p.group = a.heads / a.kv_heads, p.D = a.head_dim, p.window = a.window, p.scale = a.scale;
-  p.slots = a.q_tokens / (2 * kRows) + a.n;
+  p.heads = a.heads, p.D = a.head_dim, p.window = a.window, p.scale = a.scale;
+  p.slots = a.q_tokens / (2 * p.tile_tokens) + a.n;
   return a.head_dim <= 64 ? go<64>(mq, mk, mv, p, s) : go<128>(mq, mk, mv, p, s);
 }
 
