@@ -197,6 +197,14 @@ __device__ __forceinline__ bool wait_for(Ctl& c, unsigned long long& bar, unsign
   return false;
 }
 
+// the part of a wait that is not inlined: the phase was still open
+__device__ __noinline__ bool wait_late(Ctl& c, uint32_t bar, uint32_t parity) {
+  if (*reinterpret_cast<volatile int*>(&c.stop)) return false;
+  if (tc::mbar_wait(bar, parity, kLimitNs)) return true;
+  *reinterpret_cast<volatile int*>(&c.stop) = 1;
+  return false;
+}
+
 // the whole warp waits and goes on, or stops, together
 __device__ __forceinline__ bool warp_wait(Ctl& c, unsigned long long& bar, unsigned parity) {
   if (__all_sync(kAll, tc::mbar_try(tc::smem_u32(&bar), parity))) return true;
@@ -210,6 +218,7 @@ struct Tile {
 struct Plan {
   Tile t[2];
   int off, first, last;          // key of query r: r + off; steps of the item
+  int clean_from, clean_to;      // steps in [clean_from, clean_to) are crossed by no mask
 };
 __device__ __forceinline__ Plan plan_of(const Item& it, int tile_tokens, int window) {
   Plan p;
@@ -226,15 +235,16 @@ __device__ __forceinline__ Plan plan_of(const Item& it, int tile_tokens, int win
   }
   p.first = p.t[0].last > 0 ? p.t[0].first : p.t[1].first;
   p.last = p.t[1].last > 0 ? p.t[1].last : p.t[0].last;
+  // the diagonal of the first tile at work crosses first, the window of the last one leaves last
+  const int low = (p.t[0].last > 0 ? p.t[0].r0 : p.t[1].r0) + p.off;
+  const int high = (p.t[1].last > 0 ? p.t[1].r0 : p.t[0].r0) + tile_tokens - 1 + p.off - window;
+  p.clean_to = low >= 0 ? (low + 1) / kKeys : 0;
+  p.clean_from = window > 0 && high >= 0 ? high / kKeys + 1 : 0;
   return p;
 }
-// whether a mask crosses step j of a tile, and of any tile at work on the step
+// whether a mask crosses step j of a tile
 __device__ __forceinline__ bool crossed(const Tile& t, int off, int tile_tokens, int window, int j) {
   return (j + 1) * kKeys - 1 > t.r0 + off || (window > 0 && j * kKeys <= t.r0 + tile_tokens - 1 + off - window);
-}
-__device__ __forceinline__ bool unclean(const Plan& p, int tile_tokens, int window, int j) {
-  return (j >= p.t[0].first && j < p.t[0].last && crossed(p.t[0], p.off, tile_tokens, window, j)) ||
-         (j >= p.t[1].first && j < p.t[1].last && crossed(p.t[1], p.off, tile_tokens, window, j));
 }
 
 // One row again, by one warp: only the keys that the row sees are read
@@ -432,52 +442,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) {
         constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
         constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;      // B is N-major
-        const uint64_t dq[2] = {desc_k(sq), desc_k(sq + S::kTile)}, dk = desc_k(ring), dv = desc_n(ring);
-        auto ring_wait = [&](int u) { return wait_for(c, c.kvfull[u % S::kRing], (u / S::kRing) & 1); };
-        auto scores = [&](int i, int u, bool last) {
-          const uint64_t kk = dk + (u % S::kRing) * (S::kTile >> 4);
+        constexpr uint32_t kStep = S::kTile >> 4;
+        const uint64_t dq = desc_k(sq), dk = desc_k(ring), dv = desc_n(ring);
+        const uint32_t full = tc::smem_u32(c.kvfull), empty = tc::smem_u32(c.kvempty);
+        auto wait = [&](uint32_t bar, uint32_t parity) { return tc::mbar_try(bar, parity) || wait_late(c, bar, parity); };
+        auto scores = [&](int i, uint32_t slot, bool last) {
+          const uint64_t qq = dq + i * kStep, kk = dk + slot * kStep;
 #pragma unroll
           for (int x = 0; x < DP / 16; ++x) {
             const uint32_t o = ((x / 4) * S::kBox + (x % 4) * 32) >> 4;
-            tc::mma_bf16(s_at(i), dq[i] + o, kk + o, id_s, x > 0);
+            tc::mma_bf16(s_at(i), qq + o, kk + o, id_s, x > 0);
           }
           tc::mma_commit(tc::smem_u32(&c.sfull[i]));
           if (last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
         };
-        auto release = [&](int u) { tc::mma_commit(tc::smem_u32(&c.kvempty[u % S::kRing])); };
-        unsigned np[2] = {0, 0}, nq[2] = {0, 0}, nclean = 0;
-        int u0 = 0;                                    // the item's first K / V load
+        uint32_t np[2] = {0, 0}, nq[2] = {0, 0}, nclean = 0;               // parities of the phases to wait for
+        uint32_t slot = 0, turn = 0;                                       // the ring: next load, its parity
+        auto advance = [&]() {
+          if (++slot == S::kRing) slot = 0, turn ^= 1;
+        };
         bool ok = true;
         for (unsigned n = 0; ok; ++n) {
-          ok = wait_for(c, c.ifull[n & 1], (n / 2) & 1);
+          ok = wait(tc::smem_u32(&c.ifull[n & 1]), (n / 2) & 1);
           if (!ok) break;
           const Item it = c.item[n & 1];
           arrive(tc::smem_u32(&c.iempty[n & 1]));
           if (!it.live) break;
           const Plan p = plan_of(it, tt, window);
           if (p.last <= p.first) continue;
-          if (unclean(p, tt, window, p.first)) arrive(tc::smem_u32(&c.vgo));
-          ok = ring_wait(u0);
+          bool dirty = p.first < p.clean_from || p.first >= p.clean_to;
+          if (dirty) arrive(tc::smem_u32(&c.vgo));
+          ok = wait(full + 8 * slot, turn);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (p.t[i].last > 0 && ok) {
-              ok = wait_for(c, c.qfull[i], nq[i] & 1);
-              ++nq[i];
-              if (ok && p.t[i].first == p.first) scores(i, u0, p.t[i].last == p.first + 1);
+              ok = wait(tc::smem_u32(&c.qfull[i]), nq[i]);
+              nq[i] ^= 1;
+              if (ok && p.t[i].first == p.first) scores(i, slot, p.t[i].last == p.first + 1);
             }
-          if (ok) release(u0);
-          for (int j = p.first; j < p.last && ok; ++j) {
-            const int uv = u0 + 2 * (j - p.first) + 1, uk = uv + 1;
+          if (!ok) break;
+          tc::mma_commit(empty + 8 * slot);
+          advance();
+          for (int j = p.first; j < p.last; ++j) {
+            const uint32_t vslot = slot;
+            ok = wait(full + 8 * slot, turn);
+            advance();
             const bool more = j + 1 < p.last;
-            ok = ring_wait(uv) && (!more || ring_wait(uk));
-            if (!ok) break;
-            if (unclean(p, tt, window, j)) {
-              ok = wait_for(c, c.vclean, nclean & 1);
-              ++nclean;
-              if (!ok) break;
+            if (more && ok) ok = wait(full + 8 * slot, turn);
+            if (dirty && ok) {
+              ok = wait(tc::smem_u32(&c.vclean), nclean);
+              nclean ^= 1;
             }
-            if (more && unclean(p, tt, window, j + 1)) arrive(tc::smem_u32(&c.vgo));
-            const uint64_t vv = dv + (uv % S::kRing) * (S::kTile >> 4);
+            if (!ok) break;
+            dirty = more && (j + 1 < p.clean_from || j + 1 >= p.clean_to);
+            if (dirty) arrive(tc::smem_u32(&c.vgo));
+            const uint64_t vv = dv + vslot * kStep;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const Tile& t = p.t[i];
@@ -486,23 +505,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // while the softmax works on the others
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                  ok = ok && wait_for(c, c.pfull[i][z], np[i] & 1);
+                  ok = ok && wait(tc::smem_u32(&c.pfull[i][z]), np[i]);
                   if (!ok) break;
                   tc::fence_after_sync();
 #pragma unroll
                   for (int x = 4 * z; x < 4 * z + 4; ++x)
-                    tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, j > t.first || x > 0);
+                    tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, x > 0 || j > t.first);
                 }
-                ++np[i];
+                np[i] ^= 1;
                 if (ok && j == t.last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
               }
-              if (ok && j + 1 >= t.first && j + 1 < t.last) scores(i, uk, j + 2 == t.last);
+              if (ok && j + 1 >= t.first && j + 1 < t.last) scores(i, slot, j + 2 == t.last);
             }
             if (!ok) break;
-            release(uv);
-            if (more) release(uk);
+            tc::mma_commit(empty + 8 * vslot);
+            if (more) {
+              tc::mma_commit(empty + 8 * slot);
+              advance();
+            }
           }
-          u0 += 2 * (p.last - p.first);
         }
       }
       __syncwarp();
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int lk = it.lk;
         bool ok = true;
         for (int j = p.first; j < p.last; ++j) {
-          if (!unclean(p, tt, window, j)) continue;
+          if (j >= p.clean_from && j < p.clean_to) continue;
           // the go for step j comes when the MMA thread is one step away: the slot's
           // earlier load was consumed by then, so the parity below is of this one
           const int uv = u0 + 2 * (j - p.first) + 1;
