@@ -17,10 +17,11 @@
 //   warps 0-3, 4-7   softmax of tile 0 / tile 1: thread = row = tensor-memory lane;
 //                    at the end they scale O by 1 / l and store it (register
 //                    split: 208 each, the other four warps 88);
-//   warp 8           issues every tcgen05.mma:  PV0(j) S0(j+1) PV1(j) S1(j+1), so
-//                    the tensor cores work on one tile while the other's softmax
-//                    runs;  warp 9 loads Q, K and V by TMA (128-byte swizzle);
-//   warps 10, 11     clean the values of steps that a mask crosses (below).
+//   warps 8, 10      issue the tcgen05.mma of tile 0 / tile 1:  PV(j) S(j+1) in turn.
+//                    One thread each, so one tile's waits and bookkeeping run
+//                    under the other's products;
+//   warp 9           finds the items and loads Q, K and V by TMA (128-byte swizzle);
+//   warp 11          passes the values on, cleaned in steps that a mask crosses (below).
 // Tensor memory, 512 columns: S0 S1 (128 each, P over the first half of each)
 // and O0 O1.  MMAs execute in the order of issue, so S(j+1) may overwrite P(j)
 // right after PV(j), and a commit after S(j+1) also says that PV(j) is done.
@@ -32,7 +33,7 @@
 //
 // Masks: only tiles that the causal diagonal, the window or the sequence's end
 // crosses are masked (scores become -inf).  A weight of 0 times a value that is
-// not finite would still give NaN, so in those steps two warps zero, in shared
+// not finite would still give NaN, so in those steps a warp zeroes, in shared
 // memory, the values past the sequence's end and every value that is not finite;
 // the rows that do see such a value are computed again with plain arithmetic
 // that never touches hidden keys (redo_row).  Other rows keep their bits.
@@ -51,7 +52,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kRows = 128;                      // queries per tile
 constexpr int kKeys = 128;                      // keys per step
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kCleanWarp = 10, kTcThreads = 384;
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kCleanWarp = 11, kTcThreads = 384;   // MMA: warps 8 and 10
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 x 208 + 128 x 88 = 384 x 168, the launch's total
 constexpr float kSlack = 8.f;                   // how far (log2) weights may exceed 1 before O is rescaled
 constexpr unsigned long long kLimitNs = 2000000000ull;   // bound of every wait
@@ -60,8 +61,9 @@ template <int DP>
 struct Shape {
   static constexpr int kBox = 128 * 128;                   // bytes of 128 rows x 64 bf16
   static constexpr int kTile = kBox * (DP / 64);           // 128 rows x DP
-  static constexpr int kRing = DP == 128 ? 5 : 8;          // K / V tiles in flight
-  static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
+  static constexpr int kKeyRing = DP == 128 ? 2 : 4;       // K tiles in flight
+  static constexpr int kValRing = DP == 128 ? 3 : 4;       // V tiles in flight
+  static constexpr int kSmem = (2 + kKeyRing + kValRing) * kTile + 1024;
 };
 
 struct PromptTc {
@@ -84,14 +86,15 @@ struct Item {
 };
 
 struct Ctl {
-  unsigned long long qfull[2], qempty[2], kvfull[8], kvempty[8], sfull[2], pfull[2][2], ofull[2], vgo, vclean;
-  unsigned long long ifull[2], iempty[2], next;
+  unsigned long long qfull[2], qempty[2], kfull[4], kempty[4], vfull[4], vready[4], vempty[4];
+  unsigned long long sfull[2], pfull[2][2], ofull[2];
+  unsigned long long ifull[2], iempty[2], next, turn[2];
   __align__(16) unsigned long long cancel[2];      // what clusterlaunchcontrol answered
   Item item[2];
   uint32_t tmem;
   int stop;
 };
-constexpr int kItemReaders = 11;                   // the MMA thread, two cleaning warps, eight softmax warps
+constexpr int kItemReaders = 11;                   // two MMA threads, the cleaning warp, eight softmax warps
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -211,6 +214,15 @@ __device__ __forceinline__ bool warp_wait(Ctl& c, unsigned long long& bar, unsig
   return __all_sync(kAll, wait_for(c, bar, parity));
 }
 
+// A ring of N slots: the next one, and the parity of its next phase
+template <int N>
+struct Ring {
+  uint32_t slot = 0, turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, turn ^= 1;
+  }
+};
+
 // What a tile of 128 rows has to do: the steps [first, last) of 128 keys
 struct Tile {
   int r0, first, last;
@@ -245,6 +257,49 @@ __device__ __forceinline__ Plan plan_of(const Item& it, int tile_tokens, int win
 // whether a mask crosses step j of a tile
 __device__ __forceinline__ bool crossed(const Tile& t, int off, int tile_tokens, int window, int j) {
   return (j + 1) * kKeys - 1 > t.r0 + off || (window > 0 && j * kKeys <= t.r0 + tile_tokens - 1 + off - window);
+}
+
+// One warp: values of keys past the sequence's end, and values that are not
+// finite, become zero in a tile of 128 keys; the item notes the latter's keys.
+template <int DP>
+__device__ __forceinline__ void clean(uint32_t tile, int lane, int key0, int lk, Item& it) {
+  constexpr int kChunks = Shape<DP>::kTile / 16;               // 16 bytes: eight values of one key
+  const int valid = lk - key0;
+  // 0 * x summed up is NaN once an x is not finite: first look, then mend
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 look[4] = {zero, zero, zero, zero};
+#pragma unroll 8
+  for (int x = lane; x < kChunks; x += 32) {
+    uint32_t v[4];
+    lds128(tile + x * 16, v);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) look[y] = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v[y]), zero, look[y]);
+  }
+  look[0] = __hadd2(__hadd2(look[0], look[1]), __hadd2(look[2], look[3]));
+  const float seen = __low2float(look[0]) + __high2float(look[0]);
+  if (seen != 0.f || valid < kKeys)
+#pragma unroll 1
+    for (int x = lane; x < kChunks; x += 32) {
+      const int key = (x >> 3) & 127;
+      uint32_t v[4];
+      lds128(tile + x * 16, v);
+      bool odd = false;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if ((v[y] & 0x7f80u) == 0x7f80u) odd = true, v[y] &= 0xffff0000u;
+        if ((v[y] & 0x7f800000u) == 0x7f800000u) odd = true, v[y] &= 0x0000ffffu;
+        if (key >= valid) v[y] = 0;
+      }
+      if (odd || key >= valid)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + x * 16), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
+      if (odd && key < valid) {
+        atomicMin(&it.bad_lo, key0 + key);
+        atomicMax(&it.bad_hi, key0 + key);
+      }
+    }
+  tc::fence_async_smem();
+  __syncwarp();
 }
 
 // One row again, by one warp: only the keys that the row sees are read
@@ -295,7 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ unsigned char raw[];
   __shared__ Ctl c;
   const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t sq = base, ring = base + 2 * S::kTile;
+  const uint32_t sq = base, kring = base + 2 * S::kTile, vring = kring + S::kKeyRing * S::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tt = a.tile_tokens, window = a.window;
 
@@ -309,13 +364,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::mbar_init(tc::smem_u32(&c.ofull[i]), 1);
       tc::mbar_init(tc::smem_u32(&c.ifull[i]), 1);
       tc::mbar_init(tc::smem_u32(&c.iempty[i]), kItemReaders);
+      tc::mbar_init(tc::smem_u32(&c.turn[i]), 1);
     }
-    for (int i = 0; i < S::kRing; ++i) {
-      tc::mbar_init(tc::smem_u32(&c.kvfull[i]), 1);
-      tc::mbar_init(tc::smem_u32(&c.kvempty[i]), 1);
+    for (int i = 0; i < S::kKeyRing; ++i) {
+      tc::mbar_init(tc::smem_u32(&c.kfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.kempty[i]), 2);
     }
-    tc::mbar_init(tc::smem_u32(&c.vgo), 1);
-    tc::mbar_init(tc::smem_u32(&c.vclean), 64);
+    for (int i = 0; i < S::kValRing; ++i) {
+      tc::mbar_init(tc::smem_u32(&c.vfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.vready[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.vempty[i]), 2);
+    }
     tc::mbar_init(tc::smem_u32(&c.next), 1);
     c.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -334,7 +393,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int per_slot = a.heads / a.pack;
       int unit = blockIdx.x;
       unsigned published = 0, cancels = 0, nq[2] = {0, 0};
-      int u = 0;                                       // K / V loads so far
+      Ring<S::kKeyRing> rk;                            // the next K and V loads
+      Ring<S::kValRing> rv;
       bool ok = true;
       while (ok) {
         Item it;
@@ -377,15 +437,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tma_3d(sq + i * S::kTile + x * S::kBox, &mq, 64 * x, it.head, it.q0 + p.t[i].r0, bar);
             }
             const int kh = it.head / a.group;
-            for (int w = 0; w < 2 * (p.last - p.first) && ok; ++w) {        // K(first), then V(j), K(j + 1)
-              const int z = u % S::kRing, round = u / S::kRing;
-              if (round > 0) ok = wait_for(c, c.kvempty[z], (round - 1) & 1);
+            for (int j = p.first; j < p.last && ok; ++j) {
+              ok = wait_for(c, c.kempty[rk.slot], rk.turn ^ 1);        // a fresh slot's wait passes at once
               if (!ok) break;
-              const uint32_t bar = tc::smem_u32(&c.kvfull[z]), dst = ring + z * S::kTile;
+              uint32_t bar = tc::smem_u32(&c.kfull[rk.slot]), dst = kring + rk.slot * S::kTile;
               arrive_tx(bar, S::kTile);
-              for (int x = 0; x < DP / 64; ++x)
-                tma_3d(dst + x * S::kBox, w & 1 ? &mv : &mk, 64 * x, kh, it.k0 + (p.first + w / 2) * kKeys, bar);
-              ++u;
+              for (int x = 0; x < DP / 64; ++x) tma_3d(dst + x * S::kBox, &mk, 64 * x, kh, it.k0 + j * kKeys, bar);
+              rk.next();
+              ok = wait_for(c, c.vempty[rv.slot], rv.turn ^ 1);
+              if (!ok) break;
+              bar = tc::smem_u32(&c.vfull[rv.slot]), dst = vring + rv.slot * S::kTile;
+              arrive_tx(bar, S::kTile);
+              for (int x = 0; x < DP / 64; ++x) tma_3d(dst + x * S::kBox, &mv, 64 * x, kh, it.k0 + j * kKeys, bar);
+              rv.next();
             }
           }
           ok = __shfl_sync(kAll, ok, 0);
@@ -430,167 +494,116 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!ok && lane == 0) {                          // a wait ran out: let what is in flight land
         if (cancels > 0) tc::mbar_wait(tc::smem_u32(&c.next), (cancels - 1) & 1, kLimitNs / 8);
-        for (int w = u > S::kRing ? u - S::kRing : 0; w < u; ++w)
-          tc::mbar_wait(tc::smem_u32(&c.kvfull[w % S::kRing]), (w / S::kRing) & 1, kLimitNs / 8);
+        for (int i = 0; i < S::kKeyRing; ++i, rk.next())
+          tc::mbar_wait(tc::smem_u32(&c.kfull[rk.slot]), rk.turn ^ 1, kLimitNs / 8);
+        for (int i = 0; i < S::kValRing; ++i, rv.next())
+          tc::mbar_wait(tc::smem_u32(&c.vfull[rv.slot]), rv.turn ^ 1, kLimitNs / 8);
         for (int i = 0; i < 2; ++i)
           if (nq[i] > 0) tc::mbar_wait(tc::smem_u32(&c.qfull[i]), (nq[i] - 1) & 1, kLimitNs / 8);
       }
-    } else if (warp == kMmaWarp) {
-      // One thread runs the whole loop: a wait on a finished phase then costs some
-      // 15 cycles, where a warp that votes on it pays over 100, and the loop's own
-      // time is what keeps the tensor cores waiting.
-      if (lane == 0) {
-        constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
-        constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;      // B is N-major
-        constexpr uint32_t kStep = S::kTile >> 4;
-        const uint64_t dq = desc_k(sq), dk = desc_k(ring), dv = desc_n(ring);
-        const uint32_t full = tc::smem_u32(c.kvfull), empty = tc::smem_u32(c.kvempty);
-        auto wait = [&](uint32_t bar, uint32_t parity) { return tc::mbar_try(bar, parity) || wait_late(c, bar, parity); };
-        auto scores = [&](int i, uint32_t slot, bool last) {
-          const uint64_t qq = dq + i * kStep, kk = dk + slot * kStep;
-#pragma unroll
-          for (int x = 0; x < DP / 16; ++x) {
-            const uint32_t o = ((x / 4) * S::kBox + (x % 4) * 32) >> 4;
-            tc::mma_bf16(s_at(i), qq + o, kk + o, id_s, x > 0);
-          }
-          tc::mma_commit(tc::smem_u32(&c.sfull[i]));
-          if (last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
-        };
-        uint32_t np[2] = {0, 0}, nq[2] = {0, 0}, nclean = 0;               // parities of the phases to wait for
-        uint32_t slot = 0, turn = 0;                                       // the ring: next load, its parity
-        auto advance = [&]() {
-          if (++slot == S::kRing) slot = 0, turn ^= 1;
-        };
-        bool ok = true;
-        for (unsigned n = 0; ok; ++n) {
-          ok = wait(tc::smem_u32(&c.ifull[n & 1]), (n / 2) & 1);
-          if (!ok) break;
-          const Item it = c.item[n & 1];
-          arrive(tc::smem_u32(&c.iempty[n & 1]));
-          if (!it.live) break;
-          const Plan p = plan_of(it, tt, window);
-          if (p.last <= p.first) continue;
-          bool dirty = p.first < p.clean_from || p.first >= p.clean_to;
-          if (dirty) arrive(tc::smem_u32(&c.vgo));
-          ok = wait(full + 8 * slot, turn);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (p.t[i].last > 0 && ok) {
-              ok = wait(tc::smem_u32(&c.qfull[i]), nq[i]);
-              nq[i] ^= 1;
-              if (ok && p.t[i].first == p.first) scores(i, slot, p.t[i].last == p.first + 1);
-            }
-          if (!ok) break;
-          tc::mma_commit(empty + 8 * slot);
-          advance();
-          for (int j = p.first; j < p.last; ++j) {
-            const uint32_t vslot = slot;
-            ok = wait(full + 8 * slot, turn);
-            advance();
-            const bool more = j + 1 < p.last;
-            if (more && ok) ok = wait(full + 8 * slot, turn);
-            if (dirty && ok) {
-              ok = wait(tc::smem_u32(&c.vclean), nclean);
-              nclean ^= 1;
-            }
-            if (!ok) break;
-            dirty = more && (j + 1 < p.clean_from || j + 1 >= p.clean_to);
-            if (dirty) arrive(tc::smem_u32(&c.vgo));
-            const uint64_t vv = dv + vslot * kStep;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const Tile& t = p.t[i];
-              if (j >= t.first && j < t.last && ok) {
-                // the weights come in two halves: the first 64 keys' product runs
-                // while the softmax works on the others
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  ok = ok && wait(tc::smem_u32(&c.pfull[i][z]), np[i]);
-                  if (!ok) break;
-                  tc::fence_after_sync();
-#pragma unroll
-                  for (int x = 4 * z; x < 4 * z + 4; ++x)
-                    tc::mma_bf16_tmem_a(o_at(i), s_at(i) + 8 * x, vv + x * (2048 >> 4), id_o, x > 0 || j > t.first);
-                }
-                np[i] ^= 1;
-                if (ok && j == t.last - 1) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
-              }
-              if (ok && j + 1 >= t.first && j + 1 < t.last) scores(i, slot, j + 2 == t.last);
-            }
-            if (!ok) break;
-            tc::mma_commit(empty + 8 * vslot);
-            if (more) {
-              tc::mma_commit(empty + 8 * slot);
-              advance();
-            }
-          }
-        }
-      }
-      __syncwarp();
-    } else {
-      const int tid = threadIdx.x - 32 * kCleanWarp;           // 0 .. 63
-      unsigned ngo = 0;
-      int u0 = 0;
-      for (unsigned n = 0;; ++n) {
-        if (!warp_wait(c, c.ifull[n & 1], (n / 2) & 1)) break;
+    } else if (warp == kCleanWarp) {
+      Ring<S::kValRing> rv;
+      bool ok = true;
+      for (unsigned n = 0; ok; ++n) {
+        ok = warp_wait(c, c.ifull[n & 1], (n / 2) & 1);
+        if (!ok) break;
         Item& it = c.item[n & 1];
         if (!it.live) break;
         const Plan p = plan_of(it, tt, window);
         const int lk = it.lk;
-        bool ok = true;
         for (int j = p.first; j < p.last; ++j) {
-          if (j >= p.clean_from && j < p.clean_to) continue;
-          // the go for step j comes when the MMA thread is one step away: the slot's
-          // earlier load was consumed by then, so the parity below is of this one
-          const int uv = u0 + 2 * (j - p.first) + 1;
-          ok = warp_wait(c, c.vgo, ngo & 1) && warp_wait(c, c.kvfull[uv % S::kRing], (uv / S::kRing) & 1);
+          ok = warp_wait(c, c.vfull[rv.slot], rv.turn);
           if (!ok) break;
-          ++ngo;
-          const uint32_t vv = ring + uv % S::kRing * S::kTile;
-          const int valid = lk - j * kKeys;
-          // 0 * x summed up is NaN once an x is not finite: first look, then mend
-          __nv_bfloat162 look[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) look[y] = __floats2bfloat162_rn(0.f, 0.f);
-          const __nv_bfloat162 zero = look[0];
-#pragma unroll 8
-          for (int x = tid; x < S::kTile / 16; x += 64) {         // a 16-byte chunk: eight values of one key
-            uint32_t v[4];
-            lds128(vv + x * 16, v);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) look[y] = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v[y]), zero, look[y]);
-          }
-          look[0] = __hadd2(__hadd2(look[0], look[1]), __hadd2(look[2], look[3]));
-          const float seen = __low2float(look[0]) + __high2float(look[0]);
-          if (seen != 0.f || valid < kKeys)
-            for (int x = tid; x < S::kTile / 16; x += 64) {
-              const int key = (x >> 3) & 127;
-              uint32_t v[4];
-              lds128(vv + x * 16, v);
-              bool odd = false;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                if ((v[y] & 0x7f80u) == 0x7f80u) odd = true, v[y] &= 0xffff0000u;
-                if ((v[y] & 0x7f800000u) == 0x7f800000u) odd = true, v[y] &= 0x0000ffffu;
-                if (key >= valid) v[y] = 0;
-              }
-              if (odd || key >= valid)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(vv + x * 16), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                             : "memory");
-              if (odd && key < valid) {
-                atomicMin(&it.bad_lo, j * kKeys + key);
-                atomicMax(&it.bad_hi, j * kKeys + key);
-              }
-            }
-          tc::fence_async_smem();
-          arrive(tc::smem_u32(&c.vclean));
+          if (j < p.clean_from || j >= p.clean_to) clean<DP>(vring + rv.slot * S::kTile, lane, j * kKeys, lk, it);
+          if (lane == 0) arrive(tc::smem_u32(&c.vready[rv.slot]));
+          rv.next();
         }
-        if (!ok) break;
-        u0 += 2 * (p.last - p.first);
         __syncwarp();
-        if (lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
+        if (ok && lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
+      }
+    } else if (lane == 0) {
+      // One thread per tile runs the whole loop: a wait on a finished phase then
+      // costs some 15 cycles, where a warp that votes on it pays over 100, and the
+      // tensor cores' queue is short enough to run dry under the loop's own time.
+      constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys);
+      constexpr uint32_t id_o = tc::idesc_bf16(128, DP) | 1u << 16;        // B is N-major
+      constexpr uint32_t kStep = S::kTile >> 4;
+      const int i = warp == kMmaWarp ? 0 : 1;
+      const uint64_t dq = desc_k(sq + i * S::kTile), dk = desc_k(kring), dv = desc_n(vring);
+      const uint32_t ts = s_at(i), to = o_at(i);
+      auto wait = [&](unsigned long long& bar, uint32_t parity) {
+        return tc::mbar_try(tc::smem_u32(&bar), parity) || wait_late(c, tc::smem_u32(&bar), parity);
+      };
+      Ring<S::kKeyRing> rk;
+      Ring<S::kValRing> rv;
+      uint32_t np = 0, nq = 0, my = i ^ 1;                                 // parities of the phases to wait for
+      bool ok = true;
+      for (unsigned n = 0; ok; ++n) {
+        ok = wait(c.ifull[n & 1], (n / 2) & 1);
+        if (!ok) break;
+        const Item it = c.item[n & 1];
+        arrive(tc::smem_u32(&c.iempty[n & 1]));
+        if (!it.live) break;
+        const Plan p = plan_of(it, tt, window);
+        const int first = i ? p.t[1].first : p.t[0].first, last = i ? p.t[1].last : p.t[0].last;
+        if (last > 0) {
+          ok = wait(c.qfull[i], nq);
+          nq ^= 1;
+        }
+        // S(first .. last - 1) and PV in turn; the other steps' tiles are only passed on
+        for (int j = p.first - 1; j < p.last && ok; ++j) {
+          const bool pv = j >= first && j < last, sc = j + 1 >= first && j + 1 < last;
+          if (j >= p.first) ok = wait(c.vready[rv.slot], rv.turn) && wait(c.vfull[rv.slot], rv.turn);
+          if (j + 1 < p.last && ok) ok = wait(c.kfull[rk.slot], rk.turn);
+          // the weights come in two halves: the first 64 keys' product runs while
+          // the softmax works on the others
+          const uint64_t vv = dv + rv.slot * kStep;
+          if (pv && ok) {
+            ok = wait(c.pfull[i][0], np);
+            tc::fence_after_sync();
+            // the tiles take turns from here to the scores, so that one's products
+            // run under the other's softmax
+            if (ok) ok = wait(c.turn[i], my);
+            if (ok) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                tc::mma_bf16_tmem_a(to, ts + 8 * x, vv + x * (2048 >> 4), id_o, x > 0 || j > first);
+              ok = wait(c.pfull[i][1], np);
+              np ^= 1;
+              tc::fence_after_sync();
+            }
+          }
+          if (ok && !pv) ok = wait(c.turn[i], my);
+          my ^= 1;
+          if (!ok) break;
+          if (pv) {
+#pragma unroll
+            for (int x = 4; x < 8; ++x) tc::mma_bf16_tmem_a(to, ts + 8 * x, vv + x * (2048 >> 4), id_o, 1);
+          }
+          if (sc) {
+            const uint64_t kk = dk + rk.slot * kStep;
+#pragma unroll
+            for (int x = 0; x < DP / 16; ++x) {
+              const uint32_t o = ((x / 4) * S::kBox + (x % 4) * 32) >> 4;
+              tc::mma_bf16(ts, dq + o, kk + o, id_s, x > 0);
+            }
+            tc::mma_commit(tc::smem_u32(&c.sfull[i]));
+          }
+          arrive(tc::smem_u32(&c.turn[i ^ 1]));
+          if (j + 2 == last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
+          if (j + 1 == last && last > 0) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
+          if (j + 1 < p.last) {
+            tc::mma_commit(tc::smem_u32(&c.kempty[rk.slot]));
+            rk.next();
+          }
+          if (j >= p.first) {
+            tc::mma_commit(tc::smem_u32(&c.vempty[rv.slot]));
+            rv.next();
+          }
+        }
       }
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2;
@@ -624,19 +637,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) tie(s[x]);
         const int key = j * kKeys;
-        if (crossed(w, p.off, tt, window, j)) {
+        if ((j < p.clean_from || j >= p.clean_to) && crossed(w, p.off, tt, window, j)) {
           const int hi = at - key, lo = window > 0 ? hi - window : -1;   // seen: lo < position <= hi
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < 4; ++x) {
+            const int h = hi - 32 * x, g = lo - 32 * x;
+            uint32_t see = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+            see &= g < 0 ? ~0u : g >= 31 ? 0u : ~0u << (g + 1);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              if (32 * x + y > hi) s[x][y] = 0xff800000u;
-          if (lo >= 0) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int y = 0; y < 32; ++y)
-                if (32 * x + y <= lo) s[x][y] = 0xff800000u;
+              if (!(see >> y & 1u)) s[x][y] = 0xff800000u;
           }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -697,9 +707,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_after_sync();
       const bool mine = row < lq && row_token < tt;
       const bool some = w.last > 0 && !(l == 0.f);
-      const float f = some ? 1.f / l : 0.f;
+      const float f = !ok ? NAN : some ? 1.f / l : 0.f;
       __nv_bfloat16* to = a.out + (long long)(q0 + row) * a.out_token + head * a.out_head;
-      const bool wide = ((size_t)to & 15) == 0;
 #pragma unroll 1
       for (int x = 0; x < DP; x += 32) {
         uint32_t o[32];
@@ -708,26 +717,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ld_wait();
           tie(o);
         }
+        if (!some) {
 #pragma unroll
-        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(!ok ? NAN : some ? __uint_as_float(o[y]) * f : 0.f);
-        if (mine) {
-#pragma unroll
-          for (int y = 0; y < 32; y += 8) {
-            if (x + y >= a.D) continue;
-            const uint4 v = make_uint4(pack_bf16(__uint_as_float(o[y]), __uint_as_float(o[y + 1])),
-                                       pack_bf16(__uint_as_float(o[y + 2]), __uint_as_float(o[y + 3])),
-                                       pack_bf16(__uint_as_float(o[y + 4]), __uint_as_float(o[y + 5])),
-                                       pack_bf16(__uint_as_float(o[y + 6]), __uint_as_float(o[y + 7])));
-            if (wide) {
-              *reinterpret_cast<uint4*>(to + x + y) = v;
-            } else {
-              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int z = 0; z < 8; ++z)
-                reinterpret_cast<unsigned short*>(to)[x + y + z] = (unsigned short)(u[z / 2] >> (16 * (z & 1)));
-            }
-          }
+          for (int y = 0; y < 32; ++y) o[y] = 0u;
         }
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] = pack_bf16(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+#pragma unroll
+        for (int y = 0; y < 32; y += 8)
+          if (mine && x + y < a.D)
+            *reinterpret_cast<uint4*>(to + x + y) = make_uint4(o[y / 2], o[y / 2 + 1], o[y / 2 + 2], o[y / 2 + 3]);
       }
       tc::fence_before_sync();
       if (mine && a.lse)
@@ -813,6 +812,7 @@ cudaError_t go(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
 // cudaErrorNotSupported: a type, size or alignment that the plain kernel takes
 cudaError_t launch_attn_prompt_tc(const moe_prompt_args& a, cudaStream_t s) {
   if (a.dtype != MOE_BF16 || a.head_dim > 128 || a.k_tokens < 1 || !(a.scale > 0.f)) return cudaErrorNotSupported;
+  if (!aligned(16, a.out_d, a.out_token * 2, a.out_head * 2)) return cudaErrorNotSupported;   // 16-byte stores
   const EncodeFn fn = encoder();
   CUtensorMap mq, mk, mv;
   PromptTc p;
