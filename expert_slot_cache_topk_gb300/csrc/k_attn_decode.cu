@@ -35,21 +35,21 @@ struct Dec {
 // number of bytes for any mix of lengths, without the host knowing them.  A warp
 // that has a whole item writes its output; otherwise it leaves its maxima, sums and
 // unnormalised outputs in its two slots of the workspace (one for the item that it
-// starts in, one for the item that it ends in), and the last block of threads to
-// finish with an item joins the item's slots.  Sums are joined in the order of the
-// tokens, so results do not depend on timing.
+// starts in, one for the item that it ends in).  A block of threads joins its warps'
+// parts of an item, and where an item spans several blocks the last of them to
+// finish joins theirs.  Sums are joined in the order of the tokens, so results do
+// not depend on timing.
 //
 // Each warp keeps its own ring of blocks in shared memory, filled by 16-byte
 // asynchronous copies two or more blocks ahead (page numbers one block further
 // ahead), so no barrier runs inside the loop.  What bounds it is memory: each key
 // and value is read once per chunk of query heads.
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kMaxWarps = 12;                    // of a block of threads
 constexpr int kMaxGrid = 320;                    // blocks of threads, at most (one per SM)
 constexpr int kMaxChunk = 16;                    // query heads of an item
 
 struct Work {
-  float* slots;                  // [kMaxGrid * kWarps][2] slots of chunk * (D + 2) floats
+  float* slots;                  // [grid * warps][2] slots of chunk * (D + 2) floats, then [grid][2] of the blocks
   unsigned* arrived;             // [kMaxGrid], zero between calls
   int chunk, chunks;             // query heads per item, items per key head
 };
@@ -84,10 +84,12 @@ __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__
 template <int DP, bool SMALL>
 struct Bf16 {
   using T = __nv_bfloat16;
-  static constexpr int kBlock = 16;                                // tokens
+  static constexpr int kWarps = 12;
+  static constexpr int kBlock = DP == 128 ? 16 : 32;               // tokens
+  static constexpr int kTiles = kBlock / 8;                        // n8 tiles of the scores
   static constexpr int kRow = DP * 2;                              // bytes of a token's key in shared memory
-  static constexpr int kStage = 2 * kBlock * kRow;                 // K and V of a block
-  static constexpr int kStages = DP == 128 ? 3 : 6;
+  static constexpr int kStage = 2 * kBlock * kRow;                 // K and V of a block: 8 KB
+  static constexpr int kStages = 2;
   uint32_t q[DP / 16][4];
   float o[DP / 8][4], m[2], l[2];
 
@@ -123,36 +125,43 @@ struct Bf16 {
   // one block from shared memory; bit t of `live`: token t counts
   __device__ __forceinline__ void block(uint32_t kt, unsigned live, float scale, int lane) {
     const uint32_t vt = kt + kBlock * kRow;
-    float s[2][4];
+    float s[kTiles][4];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < kTiles; ++x)
 #pragma unroll
       for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
     const int mat = lane >> 3, mr = lane & 7;                       // ldmatrix: matrix and row of this lane's address
-    const int krow = (mat >> 1) * 8 + mr;
+    const uint32_t kbase = kt + ((mat >> 1) * 8 + mr) * kRow;
 #pragma unroll
     for (int x = 0; x < DP / 16; ++x) {
-      uint32_t b[4];
-      const uint32_t at = kt + krow * kRow + (((2 * x + (mat & 1)) ^ (krow & 7)) << 4);
-      asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                   : "r"(at));
-      mma(s[0], q[x], b[0], b[1]);
-      mma(s[1], q[x], b[2], b[3]);
+      const uint32_t col = ((2 * x + (mat & 1)) ^ mr) << 4;
+#pragma unroll
+      for (int y = 0; y < kTiles / 2; ++y) {
+        uint32_t b[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                     : "r"(kbase + y * 16 * kRow + col));
+        mma(s[2 * y], q[x], b[0], b[1]);
+        mma(s[2 * y + 1], q[x], b[2], b[3]);
+      }
     }
     const int t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+      for (int y = 0; y < (SMALL ? 2 : 4); ++y) s[x][y] *= scale;
+    if (live != (kBlock == 32 ? ~0u : (1u << (kBlock & 31)) - 1u)) {
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+        for (int y = 0; y < (SMALL ? 2 : 4); ++y)
+          if (!(live >> (8 * x + 2 * t + (y & 1)) & 1u)) s[x][y] = -INFINITY;
+    }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        if (SMALL && y >= 2) continue;
-        const bool on = live >> (8 * x + 2 * t + (y & 1)) & 1u;
-        s[x][y] = on ? s[x][y] * scale : -INFINITY;
-        mx[y >> 1] = fmaxf(mx[y >> 1], s[x][y]);
-      }
-    uint32_t p[4] = {0u, 0u, 0u, 0u};
-    float f[2] = {1.f, 1.f};
+      for (int y = 0; y < (SMALL ? 2 : 4); ++y) mx[y >> 1] = fmaxf(mx[y >> 1], s[x][y]);
 #pragma unroll
     for (int h = 0; h < (SMALL ? 1 : 2); ++h) {
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(kAll, mx[h], 1));
@@ -163,6 +172,7 @@ struct Bf16 {
     const bool grow = mx[0] > m[0] + 8.f || (m[0] == -INFINITY && mx[0] > -INFINITY) ||
                       (!SMALL && (mx[1] > m[1] + 8.f || (m[1] == -INFINITY && mx[1] > -INFINITY)));
     if (__any_sync(kAll, grow)) {
+      float f[2] = {1.f, 1.f};
 #pragma unroll
       for (int h = 0; h < (SMALL ? 1 : 2); ++h) {
         const float mn = fmaxf(m[h], mx[h]);
@@ -175,26 +185,32 @@ struct Bf16 {
 #pragma unroll
         for (int y = 0; y < (SMALL ? 2 : 4); ++y) o[x][y] *= f[y >> 1];
     }
+    uint32_t p[kTiles / 2][4];
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x) p[x / 2][2 * (x & 1) + 1] = 0u;
 #pragma unroll
     for (int h = 0; h < (SMALL ? 1 : 2); ++h) {
       const float mb = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < kTiles; ++x) {
         const float p0 = ex2(s[x][2 * h] - mb), p1 = ex2(s[x][2 * h + 1] - mb);
         l[h] += p0 + p1;
-        p[2 * x + h] = pack_bf16(p0, p1);
+        p[x / 2][2 * (x & 1) + h] = pack_bf16(p0, p1);
       }
     }
-    const int vrow = (mat & 1) * 8 + mr;
+    const uint32_t vbase = vt + ((mat & 1) * 8 + mr) * kRow;
 #pragma unroll
     for (int x = 0; x < DP / 16; ++x) {
-      uint32_t b[4];
-      const uint32_t at = vt + vrow * kRow + (((2 * x + (mat >> 1)) ^ (vrow & 7)) << 4);
-      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                   : "r"(at));
-      mma(o[2 * x], p, b[0], b[1]);
-      mma(o[2 * x + 1], p, b[2], b[3]);
+      const uint32_t col = ((2 * x + (mat >> 1)) ^ mr) << 4;
+#pragma unroll
+      for (int y = 0; y < kTiles / 2; ++y) {
+        uint32_t b[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                     : "r"(vbase + y * 16 * kRow + col));
+        mma(o[2 * x], p[y], b[0], b[1]);
+        mma(o[2 * x + 1], p[y], b[2], b[3]);
+      }
     }
   }
 
@@ -228,6 +244,7 @@ struct Bf16 {
 template <typename T_, int NC, int GC>
 struct Plain {
   using T = T_;
+  static constexpr int kWarps = 8;
   static constexpr int W = 16 / sizeof(T);
   static constexpr int kRow = NC * 128;
   static constexpr int kBlock = kRow <= 256 ? 16 : 4096 / kRow;
@@ -339,15 +356,15 @@ struct Plain {
 };
 
 template <typename Op>
-__global__ void __launch_bounds__(kThreads, 1) k_decode(const Dec a, const Work w) {
+__global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, const Work w) {
   using T = typename Op::T;
-  constexpr int kBlock = Op::kBlock;
+  constexpr int kBlock = Op::kBlock, kWarps = Op::kWarps, kThreads = kWarps * 32;
   extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ long long part[kThreads + 1];           // blocks before each thread's entries
   __shared__ struct { long long first, last; int i, hc; } rec[kWarps][2];
   __shared__ int joins;                              // the item at hand is complete: join it here
   __shared__ long long wsum[kWarps];
-  __shared__ unsigned livemask[kWarps][8];
+  __shared__ unsigned livemask[kWarps][Op::kStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = a.kv_heads * w.chunks;           // per entry
   const long long cap = (long long)a.max_pages << a.page_shift;
@@ -453,26 +470,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const Dec a, const Work 
     };
     const int units = a.D * (int)sizeof(T) / 16;     // 16-byte chunks of a token's key
     const long long head_bytes = (long long)a.D * sizeof(T) << a.page_shift;
+    constexpr int kUnits = Op::kRow / 16;            // of a row in shared memory: the rest becomes zeros
+    constexpr int kRows = kUnits < 32 ? 32 / kUnits : 1;                 // rows that the warp copies at once
     int stage = 0;
     auto load = [&](const Cursor& x, int page) {
       const bool good = (unsigned)page < (unsigned)a.num_pages;
       if (page != -2 && !good) atomicCAS(a.status, MOE_KV_OK, MOE_KV_BAD_PAGE);
-      const unsigned live = __ballot_sync(kAll, good) & ((1u << kBlock) - 1u);
+      const unsigned live = __ballot_sync(kAll, good) & (kBlock == 32 ? ~0u : (1u << (kBlock & 31)) - 1u);
       if (lane == 0) livemask[warp][stage] = live;
-      const int kh = x.hc / w.chunks;
+      // where the lane's own token is; its address is passed on to the lanes that copy it
+      const int t = x.blk * kBlock + (lane & (kBlock - 1));
+      const long long own = good ? ((long long)page * a.kv_heads + x.hc / w.chunks) * head_bytes +
+                                       (t & ((1 << a.page_shift) - 1)) * (a.D * (int)sizeof(T))
+                                 : 0;
       const uint32_t dst = my_ring + stage * Op::kStage;
-      constexpr int kUnits = Op::kRow / 16;
 #pragma unroll
       for (int y = 0; y < kBlock * kUnits / 32; ++y) {
-        const int z = lane + 32 * y, row = z / kUnits, u = z % kUnits;
-        const int pg = __shfl_sync(kAll, page, row);
+        const int row = kUnits < 32 ? lane / kUnits + y * kRows : y * 32 / kUnits;
+        const int u = kUnits < 32 ? lane % kUnits : lane + y * 32 % kUnits;
+        const long long off = __shfl_sync(kAll, own, row) + u * 16;
         const bool real = (live >> row & 1u) && u < units;
-        const long long off = real ? ((long long)pg * a.kv_heads + kh) * head_bytes +
-                                         ((x.blk * kBlock + row) & ((1 << a.page_shift) - 1)) * (a.D * (int)sizeof(T)) + u * 16
-                                   : 0;
         const uint32_t to = dst + row * Op::kRow + ((u ^ (row & 7)) << 4);
-        cp16(to, a.k + off, real);
-        cp16(to + kBlock * Op::kRow, a.v + off, real);
+        cp16(to, real ? a.k + off : a.k, real);
+        cp16(to + kBlock * Op::kRow, real ? a.v + off : a.v, real);
       }
       stage = stage + 1 == Op::kStages ? 0 : stage + 1;
     };
@@ -546,37 +566,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const Dec a, const Work 
   __threadfence();
   __syncthreads();
 
-  // join the items that this block of threads completes
+  // Items that no single warp had whole: join the block's parts, and the blocks'
+  // parts once the last of them is there.  Column pairs over threads; when there
+  // are few, groups of threads share the slots (a fixed share each, in order).
   const long long block_first = (long long)blockIdx.x * kWarps * pw;
+  float* block_slots = w.slots + (size_t)warps * 2 * slot_floats;
   for (int x = 0; x < 2 * kWarps; ++x) {
     const long long first = rec[x >> 1][x & 1].first, last = rec[x >> 1][x & 1].last;
     if (last < 0) continue;
     const long long x0 = block_first + (x >> 1) * pw;
     if (!(first >= x0 || (x == 0 && first < block_first))) continue;     // an earlier warp has the item's start
     const long long ga = first / pw, gb = (last - 1) / pw;               // the warps that hold parts of it
-    const int ca = (int)(ga / kWarps), cb = (int)(gb / kWarps);
-    __syncthreads();
-    if (tid == 0) {
-      joins = 1;
-      if (cb > ca) {
-        joins = atomicAdd(&w.arrived[ca], 1u) == (unsigned)(cb - ca);
-        if (joins) w.arrived[ca] = 0;
-      }
-      __threadfence();
-    }
-    __syncthreads();
-    if (!joins) continue;
+    const int ca = (int)(ga / kWarps), cb = (int)(gb / kWarps);          // and their blocks
     const int i = rec[x >> 1][x & 1].i, hc = rec[x >> 1][x & 1].hc;
     const int kh = hc / w.chunks, g0 = hc % w.chunks * w.chunk;
     const int rows = a.group - g0 < w.chunk ? a.group - g0 : w.chunk;
     const int pairs = rows * a.D / 2;
-    // columns over threads; when there are few, groups of threads share the slots
-    // (a fixed share each, joined in order)
-    int split = 1;
-    while (split * 2 * pairs <= kThreads && split * 2 <= gb - ga + 1) split *= 2;
-    float* sh = reinterpret_cast<float*>(ring);                          // [split][pairs][4]: m, l, o, o
-    const long long share = (gb - ga + split) / split;
-    auto put = [&](int e, float m, float l, float o0, float o1) {
+    // sums the slots q = from .. to (inclusive) at slot(q); done(column pair, m, l, o, o)
+    auto join = [&](long long from, long long to, auto&& slot, auto&& done) {
+      int split = 1;
+      while (split * 2 * pairs <= kThreads && split * 2 <= to - from + 1) split *= 2;
+      float* sh = reinterpret_cast<float*>(ring);                        // [split][pairs][4]: m, l, o, o
+      const long long share = (to - from + split) / split;
+      for (int y = tid; y < pairs * split; y += kThreads) {
+        const int sp = y / pairs, e = y % pairs, r = e / (a.D / 2), d = e % (a.D / 2) * 2;
+        const long long q0 = from + sp * share, q1 = q0 + share < to + 1 ? q0 + share : to + 1;
+        float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 8
+        for (long long q = q0; q < q1; ++q) m = fmaxf(m, __ldcg(slot(q) + w.chunk * a.D + 2 * r));
+        const float b = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+        for (long long q = q0; q < q1; ++q) {
+          const float* sl = slot(q);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(sl + w.chunk * a.D + 2 * r));
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + r * a.D + d));
+          const float f = exp2f(ml.x - b);
+          l = fmaf(ml.y, f, l), o0 = fmaf(v.x, f, o0), o1 = fmaf(v.y, f, o1);
+        }
+        if (split > 1) *reinterpret_cast<float4*>(sh + 4 * y) = make_float4(m, l, o0, o1);
+        else done(e, m, l, o0, o1);
+      }
+      if (split > 1) {
+        __syncthreads();
+        if (tid < pairs) {
+          float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+          for (int q = 0; q < split; ++q) m = fmaxf(m, sh[4 * (tid + q * pairs)]);
+          const float b = m == -INFINITY ? 0.f : m;
+          for (int q = 0; q < split; ++q) {
+            const float4 v = *reinterpret_cast<const float4*>(sh + 4 * (tid + q * pairs));
+            const float f = exp2f(v.x - b);
+            l = fmaf(v.y, f, l), o0 = fmaf(v.z, f, o0), o1 = fmaf(v.w, f, o1);
+          }
+          done(tid, m, l, o0, o1);
+        }
+      }
+    };
+    auto result = [&](int e, float m, float l, float o0, float o1) {
       const int r = e / (a.D / 2), d = e % (a.D / 2) * 2;
       T* out = (T*)a.out + i * a.out_token + (long long)(kh * a.group + g0 + r) * a.out_head + d;
       const float f = l == 0.f ? 0.f : 1.f / l;
@@ -585,44 +630,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_decode(const Dec a, const Work 
       if (d == 0 && a.lse)
         a.lse[(size_t)i * a.heads + kh * a.group + g0 + r] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
     };
-    for (int y = tid; y < pairs * split; y += kThreads) {
-      const int sp = y / pairs, e = y % pairs, r = e / (a.D / 2), d = e % (a.D / 2) * 2;
-      float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-      const long long from = ga + sp * share, to = from + share < gb + 1 ? from + share : gb + 1;
-#pragma unroll 4
-      for (long long q = from; q < to; ++q) {
-        const int z = first > q * pw ? 1 : 0;                            // the item starts inside the warp's run
-        const float* sl = w.slots + ((size_t)q * 2 + z) * slot_floats;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(sl + w.chunk * a.D + 2 * r));
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + r * a.D + d));
-        const float mn = fmaxf(m, ml.x), b = mn == -INFINITY ? 0.f : mn;
-        const float f0 = exp2f(m - b), f1 = exp2f(ml.x - b);
-        m = mn;
-        l = l * f0 + ml.y * f1, o0 = o0 * f0 + v.x * f1, o1 = o1 * f0 + v.y * f1;
-      }
-      if (split > 1) *reinterpret_cast<float4*>(sh + 4 * y) = make_float4(m, l, o0, o1);
-      else put(e, m, l, o0, o1);
+    auto warp_slot = [&](long long q) {                                  // 1: the item starts inside the warp's run
+      return w.slots + ((size_t)q * 2 + (first > q * pw ? 1 : 0)) * slot_floats;
+    };
+    auto block_slot = [&](long long q) {
+      return block_slots + ((size_t)q * 2 + (first > q * kWarps * pw ? 1 : 0)) * slot_floats;
+    };
+    __syncthreads();                                                     // the last item's shared memory is read
+    const long long lo = (long long)blockIdx.x * kWarps, hi = lo + kWarps - 1;
+    if (ca == cb) {
+      join(ga, gb, warp_slot, result);
+      continue;
     }
-    if (split > 1) {
-      __syncthreads();
-      if (tid < pairs) {
-        float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-        for (int q = 0; q < split; ++q) {
-          const float4 v = *reinterpret_cast<const float4*>(sh + 4 * (tid + q * pairs));
-          const float mn = fmaxf(m, v.x), b = mn == -INFINITY ? 0.f : mn;
-          const float f0 = exp2f(m - b), f1 = exp2f(v.x - b);
-          m = mn;
-          l = l * f0 + v.y * f1, o0 = o0 * f0 + v.z * f1, o1 = o1 * f0 + v.w * f1;
-        }
-        put(tid, m, l, o0, o1);
-      }
+    float* mine = block_slot(blockIdx.x);
+    join(ga > lo ? ga : lo, gb < hi ? gb : hi, warp_slot, [&](int e, float m, float l, float o0, float o1) {
+      const int r = e / (a.D / 2), d = e % (a.D / 2) * 2;
+      *reinterpret_cast<float2*>(mine + r * a.D + d) = make_float2(o0, o1);
+      if (d == 0) *reinterpret_cast<float2*>(mine + w.chunk * a.D + 2 * r) = make_float2(m, l);
+    });
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      joins = atomicAdd(&w.arrived[ca], 1u) == (unsigned)(cb - ca);
+      if (joins) w.arrived[ca] = 0;
+      __threadfence();
     }
+    __syncthreads();
+    if (joins) join(ca, cb, block_slot, result);
   }
 }
 
 template <typename Op>
 cudaError_t go(const Dec& a, const Work& w, cudaStream_t s) {
-  constexpr int smem = kWarps * Op::kStages * Op::kStage;
+  constexpr int smem = Op::kWarps * Op::kStages * Op::kStage;
+  static_assert(Op::kWarps <= kMaxWarps, "slots");
   static bool set[kMaxDevices] = {};
   {
     std::lock_guard<std::mutex> lock(launch_state_mutex());
@@ -635,7 +676,7 @@ cudaError_t go(const Dec& a, const Work& w, cudaStream_t s) {
     }
   }
   const int sms = device_sm_count();
-  k_decode<Op><<<sms < kMaxGrid ? sms : kMaxGrid, kThreads, smem, s>>>(a, w);
+  k_decode<Op><<<sms < kMaxGrid ? sms : kMaxGrid, Op::kWarps * 32, smem, s>>>(a, w);
   return cudaGetLastError();
 }
 
@@ -650,7 +691,7 @@ int chunk_of(int group, int most) {
 size_t attn_decode_work_bytes(const moe_kv_pages& kv, int max_heads) {
   const int group = max_heads / kv.kv_heads;
   const int chunk = group < kMaxChunk ? group : kMaxChunk;
-  return 2048 + (size_t)kMaxGrid * kWarps * 2 * chunk * (kv.head_dim + 2) * 4;
+  return 2048 + (size_t)kMaxGrid * (kMaxWarps + 1) * 2 * chunk * (kv.head_dim + 2) * 4;
 }
 
 cudaError_t launch_attn_decode(const moe_kv_pages& kv, const DecodeArgs& m, cudaStream_t s) {
