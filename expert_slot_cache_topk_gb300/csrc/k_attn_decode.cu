@@ -29,30 +29,51 @@ struct Dec {
 };
 
 // How the work is laid out.  An item is (list entry, key head, chunk of its query
-// heads); its tokens are cut into blocks (16, or fewer where a token is large).  All blocks of all items form one
-// sequence, entry by entry and head by head, and warp g of the grid takes the `pw`
-// blocks from g * pw on, whatever items they belong to: every warp streams the same
-// number of bytes for any mix of lengths, without the host knowing them.  A warp
-// that has a whole item writes its output; otherwise it leaves its maxima, sums and
-// unnormalised outputs in its two slots of the workspace (one for the item that it
-// starts in, one for the item that it ends in).  A block of threads joins its warps'
-// parts of an item, and where an item spans several blocks the last of them to
-// finish joins theirs.  Sums are joined in the order of the tokens, so results do
-// not depend on timing.
+// heads); its tokens are cut into blocks (8 KB of keys and values).  All blocks of
+// all items form one sequence, entry by entry and head by head, of which every
+// thread block gets an equal stretch, whatever items lie in it: the host need not
+// know the lengths.  A stretch is cut into runs: one for each warp, and at its end
+// as many shorter ones (kShare of it) that any warp of the grid takes by ticket
+// when it is done, because SMs differ in how fast they get memory (without tickets
+// the median SM was done at 93 us, the last at 111).
+//
+// A run that has a whole item writes its output; otherwise it leaves its maxima,
+// sums and unnormalised outputs in its two slots of the workspace (one for the item
+// that it starts in, one for the item that it ends in), and k_join, launched behind
+// it, joins an item's slots in the order of the tokens: results depend neither on
+// timing nor on who took which run.
 //
 // Each warp keeps its own ring of blocks in shared memory, filled by 16-byte
-// asynchronous copies two or more blocks ahead (page numbers one block further
-// ahead), so no barrier runs inside the loop.  What bounds it is memory: each key
-// and value is read once per chunk of query heads.
+// asynchronous copies ahead of use (page numbers one block further ahead), so no
+// barrier runs inside the loop.  What bounds it is memory: each key and value is
+// read once per chunk of query heads.
 constexpr int kMaxWarps = 12;                    // of a block of threads
-constexpr int kMaxGrid = 320;                    // blocks of threads, at most (one per SM)
+constexpr int kMaxGrid = 160;                    // blocks of threads, at most (one per SM)
 constexpr int kMaxChunk = 16;                    // query heads of an item
+constexpr int kShareNum = 1, kShareDen = 6;      // of a stretch goes to tickets
 
+// How the blocks are cut into runs; the first bytes of the workspace
+struct Cut {
+  long long all, stretch;        // blocks in all, and of a stretch
+  int warps, runs;               // of a thread block: warps, and runs of its stretch (warps or 2 * warps)
+  int pw, pc;                    // blocks of a warp's run and of a ticket run
+  unsigned ticket;               // zero between calls
+};
 struct Work {
-  float* slots;                  // [grid * warps][2] slots of chunk * (D + 2) floats, then [grid][2] of the blocks
-  unsigned* arrived;             // [kMaxGrid], zero between calls
+  Cut* cut;
+  long long* before;             // [n + 1] blocks (of one key head and chunk) before each entry
+  float* slots;                  // [runs][2] slots: chunk rows of D, then chunk pairs (m, l)
   int chunk, chunks;             // query heads per item, items per key head
 };
+__host__ __device__ constexpr int slot_size(int chunk, int D) { return (chunk * (D + 2) + 3) / 4 * 4; }
+__device__ __forceinline__ int run_of(const Cut& c, long long u) {
+  const int b = (int)(u / c.stretch), off = (int)(u - b * c.stretch), own = c.warps * c.pw;
+  return b * c.runs + (off < own ? off / c.pw : c.warps + (off - own) / c.pc);
+}
+__device__ __forceinline__ long long run_start(const Cut& c, int run) {
+  const int b = run / c.runs, k = run - b * c.runs;
+  return b * c.stretch + (k < c.warps ? k * c.pw : c.warps * c.pw + (k - c.warps) * c.pc);
+}
 
 // The item at hand and a block of it
 struct Cursor {
@@ -249,7 +270,7 @@ struct Plain {
   static constexpr int kRow = NC * 128;
   static constexpr int kBlock = kRow <= 256 ? 16 : 4096 / kRow;
   static constexpr int kStage = 2 * kBlock * kRow;
-  static constexpr int kStages = kStage <= 4096 ? 6 : 3;
+  static constexpr int kStages = 3;
   float q[GC][NC][W], o[GC][NC][W], m[GC], l[GC];
 
   __device__ __forceinline__ void start(const Dec& a, const Work& w, const Cursor& c, int lane) {
@@ -361,33 +382,38 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
   constexpr int kBlock = Op::kBlock, kWarps = Op::kWarps, kThreads = kWarps * 32;
   extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ long long part[kThreads + 1];           // blocks before each thread's entries
-  __shared__ struct { long long first, last; int i, hc; } rec[kWarps][2];
-  __shared__ int joins;                              // the item at hand is complete: join it here
   __shared__ long long wsum[kWarps];
+  __shared__ int seen_row[kThreads], seen_len[kThreads];               // entries, when a thread has one at most
   __shared__ unsigned livemask[kWarps][Op::kStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = a.kv_heads * w.chunks;           // per entry
+  const int per = (a.n + kThreads - 1) / kThreads;   // entries of a thread
   const long long cap = (long long)a.max_pages << a.page_shift;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the tokens of an entry; nothing for a row out of range
-  auto entry = [&](int i, int& row, int& from, int& len) {
+  auto fetch = [&](int i, int& row, int& len) {
     row = a.seqs[i];
     len = (unsigned)row < (unsigned)a.max_seqs ? a.lens[row] : -1;
     if (len < 0 || len > cap) {
       atomicCAS(a.status, MOE_KV_OK, MOE_KV_BAD_SEQ);
       len = 0, row = 0;
     }
+  };
+  auto entry = [&](int i, int& row, int& from, int& len) {
+    if (per == 1) row = seen_row[i], len = seen_len[i];
+    else fetch(i, row, len);
     from = a.window > 0 && len > a.window ? len - a.window : 0;
   };
   auto blocks_of = [](int from, int len) { return len > from ? (len + kBlock - 1) / kBlock - from / kBlock : 0; };
 
   // every block of threads counts all blocks: thread t the entries [t * per, (t + 1) * per)
-  const int per = (a.n + kThreads - 1) / kThreads;
   long long mine = 0;
   for (int i = tid * per; i < (tid + 1) * per && i < a.n; ++i) {
-    int row, from, len;
-    entry(i, row, from, len);
-    mine += blocks_of(from, len);
+    int row, len;
+    fetch(i, row, len);
+    if (per == 1) seen_row[i] = row, seen_len[i] = len;
+    mine += blocks_of(a.window > 0 && len > a.window ? len - a.window : 0, len);
   }
   long long scan = mine;
 #pragma unroll
@@ -397,267 +423,298 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
   }
   if (lane == 31) wsum[warp] = scan;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long base = 0, total = 0;
   for (int x = 0; x < kWarps; ++x) {
-    if (x < warp) before += wsum[x];
+    if (x < warp) base += wsum[x];
     total += wsum[x];
   }
-  part[tid] = before + scan - mine;
+  base += scan - mine;
+  part[tid] = base;
   if (tid == 0) part[kThreads] = total;
-  rec[warp][0].last = rec[warp][1].last = -1;
   __syncthreads();
-  const long long all = total * items;
-  const long long warps = (long long)gridDim.x * kWarps;
-  long long pw = (all + warps - 1) / warps;          // blocks of a warp
-  if (pw < 2) pw = 2;
 
-  // entries without tokens
-  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
-    int row, from, len;
-    entry(i, row, from, len);
-    if (len > from) continue;
-    for (int x = tid; x < a.heads * a.D; x += kThreads)
-      Elem<T>::put((T*)a.out + i * a.out_token + (x / a.D) * a.out_head + x % a.D, 0.f);
-    if (a.lse)
-      for (int h = tid; h < a.heads; h += kThreads) a.lse[(size_t)i * a.heads + h] = -INFINITY;
+  // the runs: a few blocks for each warp are not worth tickets
+  Cut cut;
+  cut.all = total * items;
+  cut.warps = kWarps;
+  const long long each = (cut.all + gridDim.x - 1) / gridDim.x;        // of a thread block
+  cut.pc = (int)(each * kShareNum / kShareDen / kWarps);
+  if (cut.pc >= Op::kStages) {                       // (so the loads are never two runs ahead of the products)
+    cut.runs = 2 * kWarps;
+    cut.pw = (int)((each - kWarps * cut.pc + kWarps - 1) / kWarps);
+    cut.stretch = kWarps * (cut.pw + cut.pc);
+  } else {
+    cut.runs = kWarps;
+    cut.pc = 1;
+    cut.pw = (int)((each + kWarps - 1) / kWarps);
+    if (cut.pw < 2) cut.pw = 2;
+    cut.stretch = kWarps * cut.pw;
+  }
+  if (blockIdx.x == 0) {                             // for k_join
+    if (tid == 0) {
+      w.cut->all = cut.all, w.cut->stretch = cut.stretch, w.cut->pw = cut.pw, w.cut->pc = cut.pc;
+      w.cut->warps = cut.warps, w.cut->runs = cut.runs;
+      w.before[a.n] = total;
+    }
+    for (int i = tid * per; i < (tid + 1) * per && i < a.n; ++i) {
+      int row, from, len;
+      entry(i, row, from, len);
+      w.before[i] = base;
+      base += blocks_of(from, len);
+    }
   }
 
-  const long long g = (long long)blockIdx.x * kWarps + warp;
-  const long long u0 = g * pw, u1 = u0 + pw < all ? u0 + pw : all;
-  const int slot_floats = w.chunk * (a.D + 2);
-  float* slots = w.slots + (size_t)g * 2 * slot_floats;
+  const uint32_t my_ring = smem_at(ring) + warp * Op::kStages * Op::kStage;
+  const int units = a.D * (int)sizeof(T) / 16;       // 16-byte chunks of a token's key
+  const long long head_bytes = (long long)a.D * sizeof(T) << a.page_shift;
+  const int slot_floats = slot_size(w.chunk, a.D);
+  const float scale = a.scale * kLog2e;
 
-  if (u0 < u1) {
-    const uint32_t my_ring = smem_at(ring) + warp * Op::kStages * Op::kStage;
-    // the cursor of the next block to load: find the entry that holds block u0
+  // A run under way: its cursor, and the blocks left in it
+  struct Run {
     Cursor c;
-    {
-      int lo = 0, hi = kThreads;                     // part[lo] * items <= u0 < part[hi] * items
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (part[mid] * items <= u0) lo = mid;
-        else hi = mid;
-      }
-      long long u = u0 - part[lo] * items;
-      c.i = lo * per;
-      for (; c.i < a.n; ++c.i) {
-        entry(c.i, c.row, c.from, c.len);
-        const long long nb = (long long)blocks_of(c.from, c.len) * items;
-        if (u < nb) break;
-        u -= nb;
-      }
-      const int nb = blocks_of(c.from, c.len);
-      c.hc = (int)(u / nb);
-      c.end = c.from / kBlock + nb;
-      c.blk = c.from / kBlock + (int)(u % nb);
+    int left, id;
+  };
+  __shared__ Run coming[kWarps];                     // start of the run being loaded, until the products get there
+  auto advance = [&](Cursor& x) {
+    if (++x.blk < x.end) return;
+    if (++x.hc == items) {
+      x.hc = 0;
+      do {
+        ++x.i;
+        entry(x.i, x.row, x.from, x.len);
+      } while (x.len <= x.from && x.i + 1 < a.n);
+      x.end = (x.len + kBlock - 1) / kBlock;
     }
-    auto advance = [&](Cursor& x) {
-      if (++x.blk < x.end) return;
-      if (++x.hc == items) {
-        x.hc = 0;
-        do {
-          ++x.i;
-          entry(x.i, x.row, x.from, x.len);
-        } while (x.len <= x.from && x.i + 1 < a.n);
-        x.end = (x.len + kBlock - 1) / kBlock;
-      }
-      x.blk = x.from / kBlock;
-    };
-    // page of token (lane % kBlock) of the cursor's block
-    auto page_of = [&](const Cursor& x) {
-      const int t = x.blk * kBlock + (lane & (kBlock - 1));
-      return t >= x.from && t < x.len ? a.table[(size_t)x.row * a.max_pages + (t >> a.page_shift)] : -2;
-    };
-    const int units = a.D * (int)sizeof(T) / 16;     // 16-byte chunks of a token's key
-    const long long head_bytes = (long long)a.D * sizeof(T) << a.page_shift;
-    constexpr int kUnits = Op::kRow / 16;            // of a row in shared memory: the rest becomes zeros
-    constexpr int kRows = kUnits < 32 ? 32 / kUnits : 1;                 // rows that the warp copies at once
-    int stage = 0;
-    auto load = [&](const Cursor& x, int page) {
-      const bool good = (unsigned)page < (unsigned)a.num_pages;
-      if (page != -2 && !good) atomicCAS(a.status, MOE_KV_OK, MOE_KV_BAD_PAGE);
-      const unsigned live = __ballot_sync(kAll, good) & (kBlock == 32 ? ~0u : (1u << (kBlock & 31)) - 1u);
-      if (lane == 0) livemask[warp][stage] = live;
-      // where the lane's own token is; its address is passed on to the lanes that copy it
-      const int t = x.blk * kBlock + (lane & (kBlock - 1));
-      const long long own = good ? ((long long)page * a.kv_heads + x.hc / w.chunks) * head_bytes +
-                                       (t & ((1 << a.page_shift) - 1)) * (a.D * (int)sizeof(T))
-                                 : 0;
-      const uint32_t dst = my_ring + stage * Op::kStage;
+    x.blk = x.from / kBlock;
+  };
+  // the next run of this warp: its own first, then by ticket
+  bool own_run = true;
+  auto next_run = [&](Run& r) {
+    long long u;
+    if (own_run) {
+      own_run = false;
+      r.id = blockIdx.x * cut.runs + warp, r.left = cut.pw;
+      u = run_start(cut, r.id);
+    } else {
+      if (cut.runs == kWarps) return false;
+      unsigned t = 0;
+      if (lane == 0) t = atomicAdd(&w.cut->ticket, 1u);
+      t = __shfl_sync(kAll, t, 0);
+      if (t >= gridDim.x * kWarps) return false;
+      r.id = t % gridDim.x * cut.runs + kWarps + t / gridDim.x, r.left = cut.pc;
+      u = run_start(cut, r.id);
+    }
+    if (u >= cut.all) return false;                  // (only the grid's last stretches are cut short)
+    if (u + r.left > cut.all) r.left = (int)(cut.all - u);
+    int lo = 0, hi = kThreads;                       // part[lo] * items <= u < part[hi] * items
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (part[mid] * items <= u) lo = mid;
+      else hi = mid;
+    }
+    u -= part[lo] * items;
+    Cursor& c = r.c;
+    for (c.i = lo * per; c.i < a.n; ++c.i) {
+      entry(c.i, c.row, c.from, c.len);
+      const long long nb = (long long)blocks_of(c.from, c.len) * items;
+      if (u < nb) break;
+      u -= nb;
+    }
+    const int nb = blocks_of(c.from, c.len);
+    c.hc = (int)(u / nb);
+    c.end = c.from / kBlock + nb;
+    c.blk = c.from / kBlock + (int)(u % nb);
+    return true;
+  };
+  // page of token (lane % kBlock) of the cursor's block
+  auto page_of = [&](const Cursor& x) {
+    const int t = x.blk * kBlock + (lane & (kBlock - 1));
+    return t >= x.from && t < x.len ? a.table[(size_t)x.row * a.max_pages + (t >> a.page_shift)] : -2;
+  };
+  constexpr int kUnits = Op::kRow / 16;              // of a row in shared memory: the rest becomes zeros
+  constexpr int kRows = kUnits < 32 ? 32 / kUnits : 1;                   // rows that the warp copies at once
+  int stage = 0;
+  auto load = [&](const Cursor& x, int page) {
+    const bool good = (unsigned)page < (unsigned)a.num_pages;
+    if (page != -2 && !good) atomicCAS(a.status, MOE_KV_OK, MOE_KV_BAD_PAGE);
+    const unsigned live = __ballot_sync(kAll, good) & (kBlock == 32 ? ~0u : (1u << (kBlock & 31)) - 1u);
+    if (lane == 0) livemask[warp][stage] = live;
+    // where the lane's own token is; its address is passed on to the lanes that copy it
+    const int t = x.blk * kBlock + (lane & (kBlock - 1));
+    const long long own = good ? ((long long)page * a.kv_heads + x.hc / w.chunks) * head_bytes +
+                                     (t & ((1 << a.page_shift) - 1)) * (a.D * (int)sizeof(T))
+                               : 0;
+    const uint32_t dst = my_ring + stage * Op::kStage;
 #pragma unroll
-      for (int y = 0; y < kBlock * kUnits / 32; ++y) {
-        const int row = kUnits < 32 ? lane / kUnits + y * kRows : y * 32 / kUnits;
-        const int u = kUnits < 32 ? lane % kUnits : lane + y * 32 % kUnits;
-        const long long off = __shfl_sync(kAll, own, row) + u * 16;
-        const bool real = (live >> row & 1u) && u < units;
-        const uint32_t to = dst + row * Op::kRow + ((u ^ (row & 7)) << 4);
-        cp16(to, real ? a.k + off : a.k, real);
-        cp16(to + kBlock * Op::kRow, real ? a.v + off : a.v, real);
-      }
-      stage = stage + 1 == Op::kStages ? 0 : stage + 1;
-    };
-    Cursor ld = c;
-    long long ul = u0;
-    int page = page_of(ld);
-    auto load_next = [&]() {
-      if (ul < u1) {
-        load(ld, page);
-        if (++ul < u1) {
-          advance(ld);
-          page = page_of(ld);
-        }
-      }
-      cp_commit();
-    };
-#pragma unroll 1
-    for (int x = 0; x < Op::kStages - 1; ++x) load_next();
-
-    Op op;
-    op.start(a, w, c, lane);
-    long long first = u0 - (c.blk - c.from / kBlock);              // the item's first block
-    long long seg = u0;                                            // the segment's
-    const float scale = a.scale * kLog2e;
-    int use = 0;
-    for (long long u = u0; u < u1; ++u) {
-      load_next();
-      cp_wait<Op::kStages - 1>();
-      __syncwarp();
-      op.block(my_ring + use * Op::kStage, livemask[warp][use], scale, lane);
-      __syncwarp();
-      use = use + 1 == Op::kStages ? 0 : use + 1;
-      const bool item_ends = c.blk + 1 == c.end;
-      if (item_ends || u + 1 == u1) {
-        const int kh = c.hc / w.chunks, g0 = c.hc % w.chunks * w.chunk;
-        const int rows = a.group - g0 < w.chunk ? a.group - g0 : w.chunk;
-        if (item_ends && seg == first) {                           // the whole item
-          T* to = (T*)a.out + c.i * a.out_token + (long long)(kh * a.group + g0) * a.out_head;
-          float* lse = a.lse ? a.lse + (size_t)c.i * a.heads + kh * a.group + g0 : nullptr;
-          op.each(rows, a.D, lane,
-                  [&](int r, int d, float x, float y, float l) {
-                    const float f = l == 0.f ? 0.f : 1.f / l;
-                    Elem<T>::put(to + r * a.out_head + d, l == 0.f ? 0.f : x * f);
-                    Elem<T>::put(to + r * a.out_head + d + 1, l == 0.f ? 0.f : y * f);
-                  },
-                  [&](int r, float m, float l) {
-                    if (lse) lse[r] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
-                  });
-        } else {
-          const int z = seg == u0 ? 0 : 1;
-          float* to = slots + z * slot_floats;
-          op.each(rows, a.D, lane,
-                  [&](int r, int d, float x, float y, float) { *reinterpret_cast<float2*>(to + r * a.D + d) = make_float2(x, y); },
-                  [&](int r, float m, float l) { *reinterpret_cast<float2*>(to + w.chunk * a.D + 2 * r) = make_float2(m, l); });
-          if (lane == 0) {
-            rec[warp][z].first = first, rec[warp][z].last = first + (c.end - c.from / kBlock);
-            rec[warp][z].i = c.i, rec[warp][z].hc = c.hc;
-          }
-        }
-        if (u + 1 < u1) {
-          advance(c);
-          op.start(a, w, c, lane);
-          first = seg = u + 1;
-        }
-      } else {
-        ++c.blk;
-      }
+    for (int y = 0; y < kBlock * kUnits / 32; ++y) {
+      const int row = kUnits < 32 ? lane / kUnits + y * kRows : y * 32 / kUnits;
+      const int u = kUnits < 32 ? lane % kUnits : lane + y * 32 % kUnits;
+      const long long off = __shfl_sync(kAll, own, row) + u * 16;
+      const bool real = (live >> row & 1u) && u < units;
+      const uint32_t to = dst + row * Op::kRow + ((u ^ (row & 7)) << 4);
+      cp16(to, real ? a.k + off : a.k, real);
+      cp16(to + kBlock * Op::kRow, real ? a.v + off : a.v, real);
     }
-    cp_wait<0>();
-  }
-  __threadfence();
-  __syncthreads();
+    stage = stage + 1 == Op::kStages ? 0 : stage + 1;
+  };
 
-  // Items that no single warp had whole: join the block's parts, and the blocks'
-  // parts once the last of them is there.  Column pairs over threads; when there
-  // are few, groups of threads share the slots (a fixed share each, in order).
-  const long long block_first = (long long)blockIdx.x * kWarps * pw;
-  float* block_slots = w.slots + (size_t)warps * 2 * slot_floats;
-  for (int x = 0; x < 2 * kWarps; ++x) {
-    const long long first = rec[x >> 1][x & 1].first, last = rec[x >> 1][x & 1].last;
-    if (last < 0) continue;
-    const long long x0 = block_first + (x >> 1) * pw;
-    if (!(first >= x0 || (x == 0 && first < block_first))) continue;     // an earlier warp has the item's start
-    const long long ga = first / pw, gb = (last - 1) / pw;               // the warps that hold parts of it
-    const int ca = (int)(ga / kWarps), cb = (int)(gb / kWarps);          // and their blocks
-    const int i = rec[x >> 1][x & 1].i, hc = rec[x >> 1][x & 1].hc;
-    const int kh = hc / w.chunks, g0 = hc % w.chunks * w.chunk;
-    const int rows = a.group - g0 < w.chunk ? a.group - g0 : w.chunk;
-    const int pairs = rows * a.D / 2;
-    // sums the slots q = from .. to (inclusive) at slot(q); done(column pair, m, l, o, o)
-    auto join = [&](long long from, long long to, auto&& slot, auto&& done) {
-      int split = 1;
-      while (split * 2 * pairs <= kThreads && split * 2 <= to - from + 1) split *= 2;
-      float* sh = reinterpret_cast<float*>(ring);                        // [split][pairs][4]: m, l, o, o
-      const long long share = (to - from + split) / split;
-      for (int y = tid; y < pairs * split; y += kThreads) {
-        const int sp = y / pairs, e = y % pairs, r = e / (a.D / 2), d = e % (a.D / 2) * 2;
-        const long long q0 = from + sp * share, q1 = q0 + share < to + 1 ? q0 + share : to + 1;
-        float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll 8
-        for (long long q = q0; q < q1; ++q) m = fmaxf(m, __ldcg(slot(q) + w.chunk * a.D + 2 * r));
-        const float b = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-        for (long long q = q0; q < q1; ++q) {
-          const float* sl = slot(q);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(sl + w.chunk * a.D + 2 * r));
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + r * a.D + d));
-          const float f = exp2f(ml.x - b);
-          l = fmaf(ml.y, f, l), o0 = fmaf(v.x, f, o0), o1 = fmaf(v.y, f, o1);
-        }
-        if (split > 1) *reinterpret_cast<float4*>(sh + 4 * y) = make_float4(m, l, o0, o1);
-        else done(e, m, l, o0, o1);
+  Run ld;                                            // being loaded
+  bool more = next_run(ld);                          // there is a block to load
+  if (!more) return;
+  Run r = ld;                                        // being worked on
+  if (lane == 0) coming[warp] = ld;
+  int page = page_of(ld.c);
+  auto load_next = [&]() {
+    if (more) {
+      load(ld.c, page);
+      if (--ld.left > 0) {
+        advance(ld.c);
+      } else {
+        more = next_run(ld);
+        if (more && lane == 0) coming[warp] = ld;
       }
-      if (split > 1) {
-        __syncthreads();
-        if (tid < pairs) {
-          float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-          for (int q = 0; q < split; ++q) m = fmaxf(m, sh[4 * (tid + q * pairs)]);
-          const float b = m == -INFINITY ? 0.f : m;
-          for (int q = 0; q < split; ++q) {
-            const float4 v = *reinterpret_cast<const float4*>(sh + 4 * (tid + q * pairs));
-            const float f = exp2f(v.x - b);
-            l = fmaf(v.y, f, l), o0 = fmaf(v.z, f, o0), o1 = fmaf(v.w, f, o1);
-          }
-          done(tid, m, l, o0, o1);
-        }
-      }
-    };
-    auto result = [&](int e, float m, float l, float o0, float o1) {
-      const int r = e / (a.D / 2), d = e % (a.D / 2) * 2;
-      T* out = (T*)a.out + i * a.out_token + (long long)(kh * a.group + g0 + r) * a.out_head + d;
-      const float f = l == 0.f ? 0.f : 1.f / l;
-      Elem<T>::put(out, l == 0.f ? 0.f : o0 * f);
-      Elem<T>::put(out + 1, l == 0.f ? 0.f : o1 * f);
-      if (d == 0 && a.lse)
-        a.lse[(size_t)i * a.heads + kh * a.group + g0 + r] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
-    };
-    auto warp_slot = [&](long long q) {                                  // 1: the item starts inside the warp's run
-      return w.slots + ((size_t)q * 2 + (first > q * pw ? 1 : 0)) * slot_floats;
-    };
-    auto block_slot = [&](long long q) {
-      return block_slots + ((size_t)q * 2 + (first > q * kWarps * pw ? 1 : 0)) * slot_floats;
-    };
-    __syncthreads();                                                     // the last item's shared memory is read
-    const long long lo = (long long)blockIdx.x * kWarps, hi = lo + kWarps - 1;
-    if (ca == cb) {
-      join(ga, gb, warp_slot, result);
+      if (more) page = page_of(ld.c);
+    }
+    cp_commit();
+  };
+#pragma unroll 1
+  for (int x = 0; x < Op::kStages - 1; ++x) load_next();
+
+  Op op;
+  int use = 0;
+  bool head = true;                                  // the segment is its run's first
+  bool from_start = r.c.blk == r.c.from / kBlock;    // and begins with its item
+  op.start(a, w, r.c, lane);
+#pragma unroll 1
+  for (;;) {
+    load_next();
+    cp_wait<Op::kStages - 1>();
+    __syncwarp();
+    op.block(my_ring + use * Op::kStage, livemask[warp][use], scale, lane);
+    __syncwarp();
+    use = use + 1 == Op::kStages ? 0 : use + 1;
+    const bool item_ends = r.c.blk + 1 == r.c.end, run_ends = --r.left == 0;
+    if (!item_ends && !run_ends) {
+      ++r.c.blk;
       continue;
     }
-    float* mine = block_slot(blockIdx.x);
-    join(ga > lo ? ga : lo, gb < hi ? gb : hi, warp_slot, [&](int e, float m, float l, float o0, float o1) {
-      const int r = e / (a.D / 2), d = e % (a.D / 2) * 2;
-      *reinterpret_cast<float2*>(mine + r * a.D + d) = make_float2(o0, o1);
-      if (d == 0) *reinterpret_cast<float2*>(mine + w.chunk * a.D + 2 * r) = make_float2(m, l);
-    });
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      joins = atomicAdd(&w.arrived[ca], 1u) == (unsigned)(cb - ca);
-      if (joins) w.arrived[ca] = 0;
-      __threadfence();
+    const int kh = r.c.hc / w.chunks, g0 = r.c.hc % w.chunks * w.chunk;
+    const int rows = a.group - g0 < w.chunk ? a.group - g0 : w.chunk;
+    if (item_ends && from_start) {                   // the whole item
+      T* to = (T*)a.out + r.c.i * a.out_token + (long long)(kh * a.group + g0) * a.out_head;
+      float* lse = a.lse ? a.lse + (size_t)r.c.i * a.heads + kh * a.group + g0 : nullptr;
+      op.each(rows, a.D, lane,
+              [&](int q, int d, float x, float y, float l) {
+                const float f = l == 0.f ? 0.f : 1.f / l;
+                Elem<T>::put(to + q * a.out_head + d, l == 0.f ? 0.f : x * f);
+                Elem<T>::put(to + q * a.out_head + d + 1, l == 0.f ? 0.f : y * f);
+              },
+              [&](int q, float m, float l) {
+                if (lse) lse[q] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+              });
+    } else {
+      float* to = w.slots + ((size_t)r.id * 2 + (head ? 0 : 1)) * slot_floats;
+      op.each(rows, a.D, lane,
+              [&](int q, int d, float x, float y, float) { *reinterpret_cast<float2*>(to + q * a.D + d) = make_float2(x, y); },
+              [&](int q, float m, float l) { *reinterpret_cast<float2*>(to + w.chunk * a.D + 2 * q) = make_float2(m, l); });
     }
-    __syncthreads();
-    if (joins) join(ca, cb, block_slot, result);
+    if (run_ends) {
+      const int done = r.id;
+      r = coming[warp];                              // the run that the loads have gone on to, if any
+      if (r.id == done) break;
+      head = true;
+    } else {
+      advance(r.c);
+      head = false;
+    }
+    from_start = r.c.blk == r.c.from / kBlock;
+    op.start(a, w, r.c, lane);
   }
+  cp_wait<0>();
+}
+
+// Joins the slots of the items that no run had whole, and writes zeros for entries
+// without tokens.  A block of threads takes one row (query head) of an item: warp x
+// the slots x, x + warps, ..., several at a time, its lanes the columns; the warps'
+// sums are then joined in order.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024) k_join(const Dec a, const Work w) {
+  __shared__ float sh[32][32 * VEC + 2];
+  const int items = a.kv_heads * w.chunks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int row = blockIdx.x % w.chunk, item = blockIdx.x / w.chunk;
+  const int i = item / items, hc = item % items;
+  const int kh = hc / w.chunks, g0 = hc % w.chunks * w.chunk;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) w.cut->ticket = 0;
+  if (g0 + row >= a.group) return;
+  const long long before = __ldcg(w.before + i), nb = __ldcg(w.before + i + 1) - before;
+  Cut cut;
+  cut.stretch = __ldcg(&w.cut->stretch), cut.pw = __ldcg(&w.cut->pw), cut.pc = __ldcg(&w.cut->pc);
+  cut.warps = __ldcg(&w.cut->warps), cut.runs = __ldcg(&w.cut->runs);
+  const long long first = before * items + hc * nb;
+  const int ra = nb ? run_of(cut, first) : 0, rb = nb ? run_of(cut, first + nb - 1) : -1;
+  if (ra == rb) return;
+  const int h = kh * a.group + g0 + row, d = lane * VEC, slot_floats = slot_size(w.chunk, a.D);
+  const bool mine = d < a.D;
+  // only the first slot can be the second one of its run: the item starts inside it
+  const int z = nb && first > run_start(cut, ra) ? 1 : 0;
+  const float* slots = w.slots + ((size_t)ra * 2) * slot_floats;
+  float m = -INFINITY, l = 0.f, o[VEC];
+#pragma unroll
+  for (int x = 0; x < VEC; ++x) o[x] = 0.f;
+  constexpr int kBatch = VEC == 2 ? 8 : VEC == 4 ? 5 : 2;
+#pragma unroll 1
+  for (int q0 = warp; q0 <= rb - ra; q0 += kBatch * warps) {
+    float2 ml[kBatch];
+    float v[kBatch][VEC];
+    float mb = m;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int q = q0 + x * warps;
+      const bool on = q <= rb - ra;
+      const float* sl = slots + (size_t)(on ? 2 * q + (q == 0 ? z : 0) : z) * slot_floats;
+      ml[x] = __ldcg(reinterpret_cast<const float2*>(sl + w.chunk * a.D + 2 * row));
+      if (!on) ml[x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int y = 0; y < VEC; y += 2) {
+        const float2 t = on && mine ? __ldcg(reinterpret_cast<const float2*>(sl + row * a.D + d + y)) : make_float2(0.f, 0.f);
+        v[x][y] = t.x, v[x][y + 1] = t.y;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) mb = fmaxf(mb, ml[x].x);
+    const float f = m == -INFINITY ? 1.f : exp2f(m - mb);       // sums under a maximum of -inf are zero, or NaN
+    m = mb, l *= f;
+#pragma unroll
+    for (int y = 0; y < VEC; ++y) o[y] *= f;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const float e = ml[x].x == -INFINITY ? 1.f : exp2f(ml[x].x - mb);
+      l = fmaf(ml[x].y, e, l);
+#pragma unroll
+      for (int y = 0; y < VEC; ++y) o[y] = fmaf(v[x][y], e, o[y]);
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < VEC; ++y) sh[warp][d + y] = o[y];
+  if (lane == 0) sh[warp][32 * VEC] = m, sh[warp][32 * VEC + 1] = l;
+  __syncthreads();
+  if (warp * 32 >= a.D) return;
+  m = lane < warps ? sh[lane][32 * VEC] : -INFINITY;
+  m = warp_max(m);
+  const float scale = lane < warps ? (sh[lane][32 * VEC] == -INFINITY ? 1.f : exp2f(sh[lane][32 * VEC] - m)) : 0.f;
+  float sum = 0.f;
+  l = 0.f;
+  for (int q = 0; q < warps; ++q) {
+    const float e = __shfl_sync(kAll, scale, q);
+    sum = fmaf(sh[q][threadIdx.x], e, sum);          // (columns past head_dim hold zeros)
+    l = fmaf(sh[q][32 * VEC + 1], e, l);
+  }
+  if (threadIdx.x < a.D)
+    Elem<T>::put((T*)a.out + i * a.out_token + (long long)h * a.out_head + threadIdx.x, l == 0.f ? 0.f : sum / l);
+  if (threadIdx.x == 0 && a.lse)
+    a.lse[(size_t)i * a.heads + h] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
 }
 
 template <typename Op>
@@ -677,7 +734,23 @@ cudaError_t go(const Dec& a, const Work& w, cudaStream_t s) {
   }
   const int sms = device_sm_count();
   k_decode<Op><<<sms < kMaxGrid ? sms : kMaxGrid, Op::kWarps * 32, smem, s>>>(a, w);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // The join starts as k_decode's blocks end and waits for all of them.  Few rows
+  // have many slots each: 32 warps; many rows have few: as many threads as columns.
+  const long long rows = (long long)a.n * a.kv_heads * w.chunks * w.chunk;
+  if (rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const int cover = (a.D + 31) / 32 * 32;            // the last join needs a thread per column
+  const int threads = rows <= 2 * sms ? 1024 : cover > 128 ? cover : 128;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows), cfg.blockDim = dim3(threads), cfg.stream = s;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  if (a.D <= 64) return cudaLaunchKernelEx(&cfg, k_join<typename Op::T, 2>, a, w);
+  if (a.D <= 128) return cudaLaunchKernelEx(&cfg, k_join<typename Op::T, 4>, a, w);
+  return cudaLaunchKernelEx(&cfg, k_join<typename Op::T, 8>, a, w);
 }
 
 // query heads of an item: the group in equal parts of at most `most`
@@ -688,10 +761,12 @@ int chunk_of(int group, int most) {
 
 }  // namespace
 
+constexpr size_t kSlotsAt = 256 + ((size_t)MOE_KV_MAX_SEQS * 8 + 255) / 256 * 256 + 256;   // cut, before, slots
+
 size_t attn_decode_work_bytes(const moe_kv_pages& kv, int max_heads) {
   const int group = max_heads / kv.kv_heads;
   const int chunk = group < kMaxChunk ? group : kMaxChunk;
-  return 2048 + (size_t)kMaxGrid * (kMaxWarps + 1) * 2 * chunk * (kv.head_dim + 2) * 4;
+  return kSlotsAt + (size_t)kMaxGrid * 2 * kMaxWarps * 2 * slot_size(chunk, kv.head_dim) * 4;
 }
 
 cudaError_t launch_attn_decode(const moe_kv_pages& kv, const DecodeArgs& m, cudaStream_t s) {
@@ -710,9 +785,9 @@ cudaError_t launch_attn_decode(const moe_kv_pages& kv, const DecodeArgs& m, cuda
   a.n = m.n, a.heads = m.heads, a.group = m.heads / kv.kv_heads, a.window = m.window, a.scale = m.scale;
   Work w;
   char* work = (char*)kv.work_d + kv_work_bytes(kv);
-  static_assert(kMaxGrid * 4 <= 2048, "arrival counts");
-  w.arrived = (unsigned*)work;
-  w.slots = (float*)(work + 2048);
+  w.cut = (Cut*)work;
+  w.before = (long long*)(work + 256);
+  w.slots = (float*)(work + kSlotsAt);
   const bool tensor = kv.dtype == MOE_BF16 && a.D <= 128;
   w.chunk = chunk_of(a.group, tensor ? kMaxChunk : a.D > 128 ? 2 : 4);
   w.chunks = (a.group + w.chunk - 1) / w.chunk;
