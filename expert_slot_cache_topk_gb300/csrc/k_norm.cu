@@ -2,10 +2,15 @@
 //   n  = b * rsqrt(mean(b^2) + eps) * post_w
 //   x' = x + res_scale * gate * n
 //   y  = x' * rsqrt(mean(x'^2) + eps) * pre_w
-// One block of threads per row (rows b, b + grid, ...): x, b and the gate are
-// read once into registers, the two means are block sums of f32 squares, and
-// x' feeds the second norm before it is rounded.  The bound is memory: x and b
-// read, x' and y written (the weights stay in registers from row to row).
+// x, b and the gate are read once, the two means are sums of f32 squares, and x'
+// feeds the second norm before it is rounded.  The bound is memory: x and b read,
+// x' and y written.
+//
+// k_norm_row: a block of threads per row, the row in registers.  One access per
+// thread (the least time for few rows), or 2 to 5 (many rows: fewer warps to a row
+// make its two sums cheaper, and more rows of an SM are in flight at once).
+// k_norm_part: short rows, 8 to 32 lanes each.  k_norm_long: rows of more than 1024
+// accesses; x' waits in shared memory.
 #include "attn_common.cuh"
 
 namespace moe {
@@ -21,141 +26,336 @@ struct NormArgs {
   float res_scale, eps;
 };
 
+// VEC elements of one access as they are in memory, and as f32
+template <typename T, int VEC>
+struct Piece {
+  uint4 u;
+  __device__ __forceinline__ void read(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      v[i] = sizeof(T) == 4 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+template <typename T>
+struct Piece<T, 1> {
+  T t;
+  __device__ __forceinline__ void read(const T* p) { t = *p; }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = Elem<T>::get(&t); }
+};
+
 // Sum over the block; `red` alternates between calls, so one barrier is enough:
 // a buffer is written again only after the barrier of the call in between,
 // which no thread passes before it has read this one.
 __device__ __forceinline__ float block_add(float v, float* red, int warps) {
   v = warp_add(v);
+  if (warps == 1) return v;
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < warps; ++w) s += red[w];
+  if (warps <= 8) {                            // all at once, in one order for every thread
+    const float4 a = *reinterpret_cast<const float4*>(red), b = *reinterpret_cast<const float4*>(red + 4);
+    float s = a.x;
+    s += warps > 1 ? a.y : 0.f, s += warps > 2 ? a.z : 0.f, s += warps > 3 ? a.w : 0.f;
+    s += warps > 4 ? b.x : 0.f, s += warps > 5 ? b.y : 0.f, s += warps > 6 ? b.z : 0.f, s += warps > 7 ? b.w : 0.f;
+    return s;
+  }
+  const int lane = threadIdx.x & 31;
+  return warp_add(lane < warps ? red[lane] : 0.f);
+}
+
+// The squares that are summed are of v / sqrt(hidden): a mean that fits f32 does
+// not overflow on the way.
+template <int VEC>
+__device__ __forceinline__ float squares(const float (&v)[VEC], float root, float s) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) s = fmaf(v[j] * root, v[j] * root, s);
   return s;
 }
 
-// VEC elements per access, NV accesses per thread: column (i * threads + t) * VEC
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024) k_norm(const NormArgs a) {
-  __shared__ float red[2][32];
-  const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
-  const int H = a.hidden;
-  const float root = rsqrtf((float)H);         // squares of v / sqrt(H) are summed: a mean that fits f32 does not overflow
-  float post[NV][VEC], pre[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * threads + t) * VEC;
-    if (c < H) {
-      if (a.post) load_vec<T, VEC>((const T*)a.post + c, post[i]);
-      if (a.y) load_vec<T, VEC>((const T*)a.pre + c, pre[i]);
-    }
-  }
+// column of a thread's access i: (i * threads + t) * VEC.  POST / GATE: with a norm
+// of the block, with a gate for every channel.
+template <typename T, int VEC, int NV, bool POST, bool GATE>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 256) k_norm_row(const NormArgs a) {
+  __shared__ __align__(16) float red[2][32];
+  const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5, H = a.hidden;
+  const float root = rsqrtf((float)H);
   int buf = 0;
   for (long long r = blockIdx.x; r < a.tokens; r += gridDim.x) {
-    float x[NV][VEC], b[NV][VEC];
+    Piece<T, VEC> bp[NV], xp[NV];
+    float x[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * threads + t) * VEC;
       if (c < H) {
-        load_vec<T, VEC>((const T*)a.x + r * a.x_row + c, x[i]);
-        if (a.block) load_vec<T, VEC>((const T*)a.block + r * a.block_row + c, b[i]);
+        if (a.block) bp[i].read((const T*)a.block + r * a.block_row + c);
+        xp[i].read((const T*)a.x + r * a.x_row + c);
       }
     }
+    float f = a.res_scale;
+    if (!GATE && a.gate) f *= Elem<T>::get((const T*)a.gate + r * a.gate_row);
     if (a.block) {
-      float f = a.res_scale;
-      if (a.post) {
+      if (POST) {
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if ((i * threads + t) * VEC < H) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fmaf(b[i][j] * root, b[i][j] * root, ss);
-          }
-        const float rs = rsqrtf(block_add(ss, red[buf], warps) + a.eps);
+        for (int i = 0; i < NV; ++i) {
+          float b[VEC];
+          bp[i].get(b);
+          if ((i * threads + t) * VEC < H) ss = squares(b, root, ss);
+        }
+        f *= rsqrtf(block_add(ss, red[buf], warps) + a.eps);
         buf ^= 1;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) b[i][j] *= rs * post[i][j];
       }
-      if (a.gate && !a.gate_col) f *= Elem<T>::get((const T*)a.gate + r * a.gate_row);
+    }
+    float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * threads + t) * VEC;
-        if (c < H) {
-          if (a.gate && a.gate_col) {
-            float g[VEC];
-            load_vec<T, VEC>((const T*)a.gate + r * a.gate_row + c, g);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * threads + t) * VEC;
+      if (c < H) {
+        xp[i].get(x[i]);
+        if (a.block) {
+          Piece<T, VEC> p;
+          float b[VEC], w[VEC];
+          bp[i].get(b);
+          if (POST) {
+            p.read((const T*)a.post + c);
+            p.get(w);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) b[i][j] *= g[j];
+            for (int j = 0; j < VEC; ++j) b[j] *= w[j];
+          }
+          if (GATE) {
+            p.read((const T*)a.gate + r * a.gate_row + c);
+            p.get(w);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) b[j] *= w[j];
           }
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) x[i][j] = fmaf(f, b[i][j], x[i][j]);
+          for (int j = 0; j < VEC; ++j) x[i][j] = fmaf(f, b[j], x[i][j]);
         }
+        if (a.x_out) store_vec<T, VEC>((T*)a.x_out + r * a.x_out_row + c, x[i]);
+        ss = squares(x[i], root, ss);
       }
     }
-    if (a.x_out) {
+    if (!a.y) continue;
+    const float rs = rsqrtf(block_add(ss, red[buf], warps) + a.eps);
+    buf ^= 1;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * threads + t) * VEC;
-        if (c < H) store_vec<T, VEC>((T*)a.x_out + r * a.x_out_row + c, x[i]);
-      }
-    }
-    if (a.y) {
-      float ss = 0.f;
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * threads + t) * VEC;
+      if (c < H) {
+        Piece<T, VEC> p;
+        float w[VEC];
+        p.read((const T*)a.pre + c);
+        p.get(w);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if ((i * threads + t) * VEC < H) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) ss = fmaf(x[i][j] * root, x[i][j] * root, ss);
-        }
-      const float rs = rsqrtf(block_add(ss, red[buf], warps) + a.eps);
-      buf ^= 1;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * threads + t) * VEC;
-        if (c < H) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) x[i][j] *= rs * pre[i][j];
-          store_vec<T, VEC>((T*)a.y + r * a.y_row + c, x[i]);
-        }
+        for (int j = 0; j < VEC; ++j) x[i][j] *= rs * w[j];
+        store_vec<T, VEC>((T*)a.y + r * a.y_row + c, x[i]);
       }
     }
   }
 }
 
-template <typename T, int VEC, int NV>
-cudaError_t go(const NormArgs& a, int threads, cudaStream_t s) {
-  // as many blocks as the SMs hold at once (2048 threads each), rows in turn
-  const long long resident = (long long)device_sm_count() * (2048 / threads > 32 ? 32 : 2048 / threads);
-  const int grid = (int)(a.tokens < resident ? a.tokens : resident);
-  k_norm<T, VEC, NV><<<grid, threads, 0, s>>>(a);
+// G lanes per row, one access each; the next row is on its way meanwhile
+template <typename T, int VEC, int G, bool POST, bool GATE>
+__global__ void __launch_bounds__(256) k_norm_part(const NormArgs a) {
+  const int t = threadIdx.x % G, c = t * VEC, H = a.hidden;
+  const long long step = (long long)gridDim.x * blockDim.x / G;
+  const bool on = c < H;
+  const float root = rsqrtf((float)H);
+  const bool same_gate = GATE && a.gate_row == 0;
+  auto sum = [&](float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  };
+  Piece<T, VEC> post, pre, gate, xn, bn;
+  float scalar = 1.f;                          // a gate for the row
+  auto fetch = [&](long long r) {
+    if (!on || r >= a.tokens) return;
+    xn.read((const T*)a.x + r * a.x_row + c);
+    if (a.block) bn.read((const T*)a.block + r * a.block_row + c);
+    if (GATE && !same_gate) gate.read((const T*)a.gate + r * a.gate_row + c);
+    if (!GATE && a.gate) scalar = Elem<T>::get((const T*)a.gate + r * a.gate_row);
+  };
+  long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / G;
+  fetch(r);
+  if (on) {
+    if (POST) post.read((const T*)a.post + c);
+    if (a.y) pre.read((const T*)a.pre + c);
+    if (same_gate) gate.read((const T*)a.gate + c);
+  }
+  for (; __any_sync(kAll, r < a.tokens); r += step) {      // the warp goes on while any of its rows is there
+    const bool live = on && r < a.tokens;
+    float x[VEC], b[VEC], g[VEC], w[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) x[j] = b[j] = 0.f, g[j] = 1.f;
+    if (live) {
+      xn.get(x);
+      if (a.block) bn.get(b);
+      if (GATE) gate.get(g);
+    }
+    float f = a.res_scale * scalar;
+    fetch(r + step);
+    if (a.block) {
+      if (POST) {
+        f *= rsqrtf(sum(squares(b, root, 0.f)) + a.eps);
+        post.get(w);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) b[j] *= w[j];
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = live ? fmaf(f, b[j] * g[j], x[j]) : 0.f;
+    }
+    if (a.x_out && live) store_vec<T, VEC>((T*)a.x_out + r * a.x_out_row + c, x);
+    if (a.y) {
+      const float rs = rsqrtf(sum(squares(x, root, 0.f)) + a.eps);
+      if (live) {
+        pre.get(w);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] *= rs * w[j];
+        store_vec<T, VEC>((T*)a.y + r * a.y_row + c, x);
+      }
+    }
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a) {
+  __shared__ __align__(16) float red[2][32];
+  extern __shared__ float keep[];              // x' of the row
+  const int H = a.hidden, warps = blockDim.x >> 5, step = blockDim.x * VEC;
+  const float root = rsqrtf((float)H);
+  int buf = 0;
+  for (long long r = blockIdx.x; r < a.tokens; r += gridDim.x) {
+    const T* xr = (const T*)a.x + r * a.x_row;
+    const T* br = (const T*)a.block + r * a.block_row;
+    const T* gr = (const T*)a.gate + r * a.gate_row;
+    float rs = 1.f, ss = 0.f;
+    if (a.post) {
+#pragma unroll 4
+      for (int c = threadIdx.x * VEC; c < H; c += step) {
+        Piece<T, VEC> p;
+        float b[VEC];
+        p.read(br + c);
+        p.get(b);
+        ss = squares(b, root, ss);
+      }
+      rs = rsqrtf(block_add(ss, red[buf], warps) + a.eps);
+      buf ^= 1;
+    }
+    const float f = rs * a.res_scale * (a.gate && !a.gate_col ? Elem<T>::get(gr) : 1.f);
+    ss = 0.f;
+#pragma unroll 2
+    for (int c = threadIdx.x * VEC; c < H; c += step) {
+      Piece<T, VEC> p;
+      float x[VEC], b[VEC], w[VEC];
+      p.read(xr + c);
+      p.get(x);
+      if (a.block) {
+        p.read(br + c);
+        p.get(b);
+        if (a.post) {
+          p.read((const T*)a.post + c);
+          p.get(w);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) b[j] *= w[j];
+        }
+        if (a.gate && a.gate_col) {
+          p.read(gr + c);
+          p.get(w);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) b[j] *= w[j];
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] = fmaf(f, b[j], x[j]);
+      }
+      if (a.x_out) store_vec<T, VEC>((T*)a.x_out + r * a.x_out_row + c, x);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) keep[c + j] = x[j];
+      ss = squares(x, root, ss);
+    }
+    if (!a.y) continue;                        // (a thread reads back its own part of keep only)
+    rs = rsqrtf(block_add(ss, red[buf], warps) + a.eps);
+    buf ^= 1;
+#pragma unroll 2
+    for (int c = threadIdx.x * VEC; c < H; c += step) {
+      Piece<T, VEC> p;
+      float x[VEC], w[VEC];
+      p.read((const T*)a.pre + c);
+      p.get(w);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = keep[c + j] * rs * w[j];
+      store_vec<T, VEC>((T*)a.y + r * a.y_row + c, x);
+    }
+  }
+}
+
+// As many blocks as are resident at once, at most one for `rows` rows
+template <typename K>
+cudaError_t launch(K* kernel, const NormArgs& a, int threads, size_t smem, int rows, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const long long want = (a.tokens + rows - 1) / rows;
+  long long grid = want;
+  if (want > device_sm_count()) {
+    int per_sm = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    const long long resident = (long long)device_sm_count() * (per_sm > 0 ? per_sm : 1);
+    grid = want < resident ? want : resident;
+  }
+  kernel<<<(unsigned)grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t pick(const NormArgs& a, bool vec, cudaStream_t s) {
-  constexpr int W = 16 / sizeof(T);
-  const int chunks = vec ? a.hidden / W : a.hidden;
-  // one access per thread up to 512 threads, then more accesses per thread
-  int nv = 1;
-  while (chunks > nv * (nv < 4 ? 512 : 1024) && nv < 32) nv *= 2;
-  const int threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
-  if (vec) {
-    switch (nv) {
-      case 1: return go<T, W, 1>(a, threads, s);
-      case 2: return go<T, W, 2>(a, threads, s);
-      case 4: return go<T, W, 4>(a, threads, s);
-      default: return go<T, W, 8>(a, threads, s);
+template <typename T, int VEC, int NV>
+cudaError_t by_row(const NormArgs& a, int threads, cudaStream_t s) {
+  const bool gate = a.gate && a.gate_col;
+  if (a.post)
+    return gate ? launch(k_norm_row<T, VEC, NV, true, true>, a, threads, 0, 1, s)
+                : launch(k_norm_row<T, VEC, NV, true, false>, a, threads, 0, 1, s);
+  return gate ? launch(k_norm_row<T, VEC, NV, false, true>, a, threads, 0, 1, s)
+              : launch(k_norm_row<T, VEC, NV, false, false>, a, threads, 0, 1, s);
+}
+
+template <typename T, int VEC, int G>
+cudaError_t by_part(const NormArgs& a, cudaStream_t s) {
+  const bool gate = a.gate && a.gate_col;
+  if (a.post)
+    return gate ? launch(k_norm_part<T, VEC, G, true, true>, a, 256, 0, 256 / G, s)
+                : launch(k_norm_part<T, VEC, G, true, false>, a, 256, 0, 256 / G, s);
+  return gate ? launch(k_norm_part<T, VEC, G, false, true>, a, 256, 0, 256 / G, s)
+              : launch(k_norm_part<T, VEC, G, false, false>, a, 256, 0, 256 / G, s);
+}
+
+template <typename T, int VEC>
+cudaError_t pick(const NormArgs& a, cudaStream_t s) {
+  const int chunks = a.hidden / VEC;
+  if (chunks > 1024) return launch(k_norm_long<T, VEC>, a, 1024, (size_t)a.hidden * 4, 1, s);
+  if (chunks <= 8) return by_part<T, VEC, 8>(a, s);
+  if (chunks <= 16) return by_part<T, VEC, 16>(a, s);
+  if (chunks <= 32) return by_part<T, VEC, 32>(a, s);
+  if constexpr (VEC > 1) {
+    // Enough rows to give every SM several: the accesses per thread that leave the
+    // fewest of a row's threads idle, the more the better
+    if (a.tokens >= 8ll * device_sm_count()) {
+      int best = 1, idle = 1 << 30;
+      for (int nv = 5; nv >= 2; --nv) {
+        const int warps = (chunks + 32 * nv - 1) / (32 * nv);
+        if (warps <= 8 && warps * 32 * nv - chunks < idle) best = nv, idle = warps * 32 * nv - chunks;
+      }
+      const int threads = (chunks + 32 * best - 1) / (32 * best) * 32;
+      switch (best) {
+        case 5: return by_row<T, VEC, 5>(a, threads, s);
+        case 4: return by_row<T, VEC, 4>(a, threads, s);
+        case 3: return by_row<T, VEC, 3>(a, threads, s);
+        case 2: return by_row<T, VEC, 2>(a, threads, s);
+      }
     }
   }
-  switch (nv) {
-    case 1: return go<T, 1, 1>(a, threads, s);
-    case 2: return go<T, 1, 2>(a, threads, s);
-    case 4: return go<T, 1, 4>(a, threads, s);
-    case 8: return go<T, 1, 8>(a, threads, s);
-    case 16: return go<T, 1, 16>(a, threads, s);
-    default: return go<T, 1, 32>(a, threads, s);
-  }
+  return by_row<T, VEC, 1>(a, (chunks + 31) / 32 * 32, s);
 }
 
 }  // namespace
@@ -173,7 +373,8 @@ cudaError_t launch_norm(const moe_norm_args& m, cudaStream_t s) {
   const bool vec = aligned(16, m.x_d, m.block_d, m.post_w_d, m.pre_w_d, m.x_out_d, m.y_d, m.hidden * e, m.x_row * e,
                            m.block_row * e, m.x_out_row * e, m.y_row * e) &&
                    (!m.gate_d || !m.gate_col || aligned(16, m.gate_d, m.gate_row * e));
-  return m.dtype == MOE_BF16 ? pick<__nv_bfloat16>(a, vec, s) : pick<float>(a, vec, s);
+  if (m.dtype == MOE_BF16) return vec ? pick<__nv_bfloat16, 8>(a, s) : pick<__nv_bfloat16, 1>(a, s);
+  return vec ? pick<float, 4>(a, s) : pick<float, 1>(a, s);
 }
 
 }  // namespace moe
