@@ -11,6 +11,8 @@
 // make its two sums cheaper, and more rows of an SM are in flight at once).
 // k_norm_part: short rows, 8 to 32 lanes each.  k_norm_long: rows of more than 1024
 // accesses; x' waits in shared memory.
+#include <atomic>
+
 #include "attn_common.cuh"
 
 namespace moe {
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 256) k_norm_row(const NormArg
   const float root = rsqrtf((float)H);
   int buf = 0;
   for (long long r = blockIdx.x; r < a.tokens; r += gridDim.x) {
-    Piece<T, VEC> bp[NV], xp[NV];
+    Piece<T, VEC> bp[NV], xp[NV], gp[NV];
     float x[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -90,6 +92,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 256) k_norm_row(const NormArg
       if (c < H) {
         if (a.block) bp[i].read((const T*)a.block + r * a.block_row + c);
         xp[i].read((const T*)a.x + r * a.x_row + c);
+        if (GATE) gp[i].read((const T*)a.gate + r * a.gate_row + c);
       }
     }
     float f = a.res_scale;
@@ -124,8 +127,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 256) k_norm_row(const NormArg
             for (int j = 0; j < VEC; ++j) b[j] *= w[j];
           }
           if (GATE) {
-            p.read((const T*)a.gate + r * a.gate_row + c);
-            p.get(w);
+            gp[i].get(w);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) b[j] *= w[j];
           }
@@ -291,22 +293,32 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a) {
 }
 
 // As many blocks as are resident at once, at most one for `rows` rows
-template <typename K>
-cudaError_t launch(K* kernel, const NormArgs& a, int threads, size_t smem, int rows, cudaStream_t s) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+template <auto kKernel>
+cudaError_t launch(const NormArgs& a, int threads, size_t smem, int rows, cudaStream_t s) {
   const long long want = (a.tokens + rows - 1) / rows;
   long long grid = want;
-  if (want > device_sm_count()) {
-    int per_sm = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const long long resident = (long long)device_sm_count() * (per_sm > 0 ? per_sm : 1);
+  }
+  if (want > device_sm_count()) {
+    // the last answer of the occupancy query (threads, shared memory, blocks) is kept for each device
+    static std::atomic<unsigned long long> known[kMaxDevices] = {};
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    const unsigned long long key = (unsigned long long)threads << 40 | (unsigned long long)smem << 8;
+    unsigned long long got = known[dev].load(std::memory_order_relaxed);
+    if ((got & ~255ull) != key) {
+      int per_sm = 0;
+      const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kKernel, threads, smem);
+      if (e != cudaSuccess) return e;
+      got = key | (unsigned)(per_sm > 0 ? per_sm : 1);
+      known[dev].store(got, std::memory_order_relaxed);
+    }
+    const long long resident = (long long)device_sm_count() * (long long)(got & 255);
     grid = want < resident ? want : resident;
   }
-  kernel<<<(unsigned)grid, threads, smem, s>>>(a);
+  kKernel<<<(unsigned)grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -314,26 +326,26 @@ template <typename T, int VEC, int NV>
 cudaError_t by_row(const NormArgs& a, int threads, cudaStream_t s) {
   const bool gate = a.gate && a.gate_col;
   if (a.post)
-    return gate ? launch(k_norm_row<T, VEC, NV, true, true>, a, threads, 0, 1, s)
-                : launch(k_norm_row<T, VEC, NV, true, false>, a, threads, 0, 1, s);
-  return gate ? launch(k_norm_row<T, VEC, NV, false, true>, a, threads, 0, 1, s)
-              : launch(k_norm_row<T, VEC, NV, false, false>, a, threads, 0, 1, s);
+    return gate ? launch<k_norm_row<T, VEC, NV, true, true>>(a, threads, 0, 1, s)
+                : launch<k_norm_row<T, VEC, NV, true, false>>(a, threads, 0, 1, s);
+  return gate ? launch<k_norm_row<T, VEC, NV, false, true>>(a, threads, 0, 1, s)
+              : launch<k_norm_row<T, VEC, NV, false, false>>(a, threads, 0, 1, s);
 }
 
 template <typename T, int VEC, int G>
 cudaError_t by_part(const NormArgs& a, cudaStream_t s) {
   const bool gate = a.gate && a.gate_col;
   if (a.post)
-    return gate ? launch(k_norm_part<T, VEC, G, true, true>, a, 256, 0, 256 / G, s)
-                : launch(k_norm_part<T, VEC, G, true, false>, a, 256, 0, 256 / G, s);
-  return gate ? launch(k_norm_part<T, VEC, G, false, true>, a, 256, 0, 256 / G, s)
-              : launch(k_norm_part<T, VEC, G, false, false>, a, 256, 0, 256 / G, s);
+    return gate ? launch<k_norm_part<T, VEC, G, true, true>>(a, 256, 0, 256 / G, s)
+                : launch<k_norm_part<T, VEC, G, true, false>>(a, 256, 0, 256 / G, s);
+  return gate ? launch<k_norm_part<T, VEC, G, false, true>>(a, 256, 0, 256 / G, s)
+              : launch<k_norm_part<T, VEC, G, false, false>>(a, 256, 0, 256 / G, s);
 }
 
 template <typename T, int VEC>
 cudaError_t pick(const NormArgs& a, cudaStream_t s) {
   const int chunks = a.hidden / VEC;
-  if (chunks > 1024) return launch(k_norm_long<T, VEC>, a, 1024, (size_t)a.hidden * 4, 1, s);
+  if (chunks > 1024) return launch<k_norm_long<T, VEC>>(a, 1024, (size_t)a.hidden * 4, 1, s);
   if (chunks <= 8) return by_part<T, VEC, 8>(a, s);
   if (chunks <= 16) return by_part<T, VEC, 16>(a, s);
   if (chunks <= 32) return by_part<T, VEC, 32>(a, s);
