@@ -254,11 +254,6 @@ __device__ __forceinline__ Plan plan_of(const Item& it, int tile_tokens, int win
   p.clean_from = window > 0 && high >= 0 ? high / kKeys + 1 : 0;
   return p;
 }
-// whether a mask crosses step j of a tile
-__device__ __forceinline__ bool crossed(const Tile& t, int off, int tile_tokens, int window, int j) {
-  return (j + 1) * kKeys - 1 > t.r0 + off || (window > 0 && j * kKeys <= t.r0 + tile_tokens - 1 + off - window);
-}
-
 // One warp: values of keys past the sequence's end, and values that are not
 // finite, become zero in a tile of 128 keys; the item notes the latter's keys.
 template <int DP>
@@ -609,6 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int i = warp >> 2;
     const uint32_t quad = (uint32_t)(warp & 3) * 32u << 16;
     const int in_tile = (warp & 3) * 32 + lane;             // the thread's row of the tile
+    const int quarter = lane & 3;
     const int row_token = in_tile / a.pack, row_head = in_tile - row_token * a.pack;
     const float sc = a.scale * kLog2e;
     const unsigned long long sc2 = pair(sc, sc);
@@ -637,10 +633,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) tie(s[x]);
         const int key = j * kKeys;
-        if ((j < p.clean_from || j >= p.clean_to) && crossed(w, p.off, tt, window, j)) {
+        if (j < p.clean_from || j >= p.clean_to) {
           const int hi = at - key, lo = window > 0 ? hi - window : -1;   // seen: lo < position <= hi
+          // the last row's and the first row's bounds: 32 keys that all rows of the warp
+          // see need no look at single ones
+          const int hi1 = __shfl_sync(kAll, hi, 31), hi0 = __shfl_sync(kAll, hi, 0);
+          const int lo1 = window > 0 ? hi1 - window : -1;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
+            if (32 * x + 31 <= hi0 && 32 * x > lo1) continue;
             const int h = hi - 32 * x, g = lo - 32 * x;
             uint32_t see = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
             see &= g < 0 ? ~0u : g >= 31 ? 0u : ~0u << (g + 1);
@@ -708,7 +709,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool mine = row < lq && row_token < tt;
       const bool some = w.last > 0 && !(l == 0.f);
       const float f = !ok ? NAN : some ? 1.f / l : 0.f;
-      __nv_bfloat16* to = a.out + (long long)(q0 + row) * a.out_token + head * a.out_head;
+      // the rows of the quad: row quarter ^ y of it, null where there is none
+      __nv_bfloat16* to[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int rr = __shfl_xor_sync(kAll, row, y), hh = __shfl_xor_sync(kAll, head, y);
+        to[y] = __shfl_xor_sync(kAll, (int)mine, y) ? a.out + (long long)(q0 + rr) * a.out_token + hh * a.out_head : nullptr;
+      }
 #pragma unroll 1
       for (int x = 0; x < DP; x += 32) {
         uint32_t o[32];
@@ -723,10 +730,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
 #pragma unroll
         for (int y = 0; y < 16; ++y) o[y] = pack_bf16(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+        // The four lanes of a quad exchange 16-byte pieces, so that each store writes 64
+        // bytes of eight rows instead of 16 bytes of 32: lane q of the quad gets piece q
+        // of every row of the quad, row q ^ y in piece y.
+        uint32_t v[4][4];
 #pragma unroll
-        for (int y = 0; y < 32; y += 8)
-          if (mine && x + y < a.D)
-            *reinterpret_cast<uint4*>(to + x + y) = make_uint4(o[y / 2], o[y / 2 + 1], o[y / 2 + 2], o[y / 2 + 3]);
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const uint32_t low = quarter & 1 ? o[4 * (y ^ 1) + z] : o[4 * y + z];            // piece quarter ^ y, bit 0 settled
+            const uint32_t high = quarter & 1 ? o[4 * (y ^ 3) + z] : o[4 * (y ^ 2) + z];
+            v[y][z] = quarter & 2 ? high : low;
+          }
+#pragma unroll
+        for (int y = 1; y < 4; ++y)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) v[y][z] = __shfl_xor_sync(kAll, v[y][z], y);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (to[y] && x + 8 * quarter < a.D)
+            *reinterpret_cast<uint4*>(to[y] + x + 8 * quarter) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
       }
       tc::fence_before_sync();
       if (mine && a.lse)
