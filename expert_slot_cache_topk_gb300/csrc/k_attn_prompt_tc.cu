@@ -13,15 +13,15 @@
 // item, so the next item's loads and first products run under this one's end,
 // and late tiles (the long ones under the causal mask) are handed out first.
 //
-// Warp roles (12 warps, one block per SM):
+// Warp roles (16 warps, one block per SM, registers split as their work needs):
 //   warps 0-3, 4-7   softmax of tile 0 / tile 1: thread = row = tensor-memory lane;
-//                    at the end they scale O by 1 / l and store it (register
-//                    split: 208 each, the other four warps 88);
 //   warps 8, 10      issue the tcgen05.mma of tile 0 / tile 1:  PV(j) S(j+1) in turn.
 //                    One thread each, so one tile's waits and bookkeeping run
 //                    under the other's products;
 //   warp 9           finds the items and loads Q, K and V by TMA (128-byte swizzle);
-//   warp 11          passes the values on, cleaned in steps that a mask crosses (below).
+//   warp 11          passes the values on, cleaned in steps that a mask crosses (below);
+//   warps 12-15      scale both tiles' O by 1 / l and store them, while the softmax
+//                    warps are at the next item.
 // Tensor memory, 512 columns: S0 S1 (128 each, P over the first half of each)
 // and O0 O1.  MMAs execute in the order of issue, so S(j+1) may overwrite P(j)
 // right after PV(j), and a commit after S(j+1) also says that PV(j) is done.
@@ -52,18 +52,20 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kRows = 128;                      // queries per tile
 constexpr int kKeys = 128;                      // keys per step
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kCleanWarp = 11, kTcThreads = 384;   // MMA: warps 8 and 10
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 x 208 + 128 x 88 = 384 x 168, the launch's total
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kCleanWarp = 11, kEndWarp = 12, kTcThreads = 512;   // MMA: warps 8 and 10
+// 256 x 192 + 128 x 56 + 128 x 72 = 512 x 128, the launch's total
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 56, kEndRegs = 72;
 constexpr float kSlack = 8.f;                   // how far (log2) weights may exceed 1 before O is rescaled
 constexpr unsigned long long kLimitNs = 2000000000ull;   // bound of every wait
 
+constexpr int kCtl = 3072;                      // barriers, items and row sums in front of the tiles
 template <int DP>
 struct Shape {
   static constexpr int kBox = 128 * 128;                   // bytes of 128 rows x 64 bf16
   static constexpr int kTile = kBox * (DP / 64);           // 128 rows x DP
   static constexpr int kKeyRing = DP == 128 ? 2 : 4;       // K tiles in flight
   static constexpr int kValRing = DP == 128 ? 3 : 4;       // V tiles in flight
-  static constexpr int kSmem = (2 + kKeyRing + kValRing) * kTile + 1024;
+  static constexpr int kSmem = kCtl + (2 + kKeyRing + kValRing) * kTile;   // 227 KB, all there is, for head sizes past 64
 };
 
 struct PromptTc {
@@ -87,14 +89,16 @@ struct Item {
 
 struct Ctl {
   unsigned long long qfull[2], qempty[2], kfull[4], kempty[4], vfull[4], vready[4], vempty[4];
-  unsigned long long sfull[2], pfull[2][2], ofull[2];
+  unsigned long long sfull[2], pfull[2][2], ofull[2], oempty[2], lfull[2], lempty[2];
   unsigned long long ifull[2], iempty[2], next, turn[2];
   __align__(16) unsigned long long cancel[2];      // what clusterlaunchcontrol answered
   Item item[2];
+  float weight[32];              // of redo_row
+  float2 sums[2][128];           // [tile][row]: m and l of finished rows
   uint32_t tmem;
   int stop;
 };
-constexpr int kItemReaders = 11;                   // two MMA threads, the cleaning warp, eight softmax warps
+constexpr int kItemReaders = 15;                   // two MMA threads, the cleaning warp, eight softmax and four storing warps
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -167,21 +171,27 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // arithmetic on r stays behind the statements before this one
-__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void tie(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -212,6 +222,13 @@ __device__ __noinline__ bool wait_late(Ctl& c, uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool warp_wait(Ctl& c, unsigned long long& bar, unsigned parity) {
   if (__all_sync(kAll, tc::mbar_try(tc::smem_u32(&bar), parity))) return true;
   return __all_sync(kAll, wait_for(c, bar, parity));
+}
+
+// the first key that a query whose last key is `at` sees, and whether it sees a
+// value that was zeroed (with several such keys, one between them counts as well)
+__device__ __forceinline__ int first_key(int at, int window) { return window > 0 && at >= window ? at - window + 1 : 0; }
+__device__ __forceinline__ bool sees_zeroed(const Item& it, int at, int window) {
+  return it.bad_hi >= first_key(at, window) && it.bad_lo <= at;
 }
 
 // A ring of N slots: the next one, and the parity of its next phase
@@ -297,44 +314,46 @@ __device__ __forceinline__ void clean(uint32_t tile, int lane, int key0, int lk,
   __syncwarp();
 }
 
-// One row again, by one warp: only the keys that the row sees are read
-__device__ __noinline__ void redo_row(const PromptTc& a, int h, int q_at, long long k_first, int count) {
+// One row again, by one warp: only the keys that the row sees are read.  Three
+// passes (maximum, sum, then one column at a time per lane) need few registers.
+__device__ __noinline__ void redo_row(const PromptTc& a, int h, int q_at, long long k_first, int count, float* weight) {
   const int lane = threadIdx.x & 31;
   const __nv_bfloat16* q = a.q + q_at * a.q_token + h * a.q_head;
   const __nv_bfloat16* k = a.k + k_first * a.k_token + (long long)(h / a.group) * a.k_head;
+  auto score = [&](int j) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < a.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[j * a.k_token + d]), s);
+    return s * a.scale * kLog2e;
+  };
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int j = lane; j < count; j += 32) m = fmaxf(m, score(j));
+  m = warp_max(m);
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+  for (int j = lane; j < count; j += 32) l += exp2f(score(j) - base);
+  l = warp_add(l);
   const __nv_bfloat16* v = a.v + k_first * a.v_token + (long long)(h / a.group) * a.v_head;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 < count; j0 += 32) {
-    float s = -INFINITY;
-    if (j0 + lane < count) {
-      s = 0.f;
-      for (int d = 0; d < a.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[(j0 + lane) * a.k_token + d]), s);
-      s *= a.scale * kLog2e;
+#pragma unroll 1
+  for (int d0 = 0; d0 < a.D; d0 += 32) {
+    float o = 0.f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < count; j0 += 32) {
+      __syncwarp();
+      weight[lane] = j0 + lane < count ? exp2f(score(j0 + lane) - base) : 0.f;
+      __syncwarp();
+#pragma unroll 1
+      for (int j = 0; j < 32 && j0 + j < count; ++j) {
+        const float w = weight[j];
+        if (d0 + lane < a.D) o = fmaf(w, __bfloat162float(v[(j0 + j) * a.v_token + d0 + lane]), o);
+      }
     }
-    const float mn = fmaxf(m, warp_max(s)), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m - base);
-    const float p = j0 + lane < count ? exp2f(s - base) : 0.f;
-    m = mn;
-    l = l * f + warp_add(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= f;
-    for (int j = 0; j < 32 && j0 + j < count; ++j) {
-      const float w = __shfl_sync(kAll, p, j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < a.D) o[i] = fmaf(w, __bfloat162float(v[(j0 + j) * a.v_token + lane + 32 * i]), o[i]);
-    }
-    bool lost = true;                                      // every sum is NaN: it stays so
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lost = lost && (lane + 32 * i >= a.D || o[i] != o[i]);
-    if (__all_sync(kAll, lost) && l != l) break;
+    if (d0 + lane < a.D)
+      a.out[q_at * a.out_token + h * a.out_head + d0 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
   }
-  const bool some = !(l == 0.f);
-  __nv_bfloat16* to = a.out + q_at * a.out_token + h * a.out_head;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < a.D) to[lane + 32 * i] = __float2bfloat16_rn(some ? o[i] / l : 0.f);
   if (lane == 0 && a.lse)
-    a.lse[(long long)q_at * a.heads + h] = some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
+    a.lse[(long long)q_at * a.heads + h] = l == 0.f ? -INFINITY : base * kLn2 + logf(l);
 }
 
 template <int DP>
@@ -342,9 +361,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     k_prompt_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptTc a) {
   using S = Shape<DP>;
-  extern __shared__ unsigned char raw[];
-  __shared__ Ctl c;
-  const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  Ctl& c = *reinterpret_cast<Ctl*>(raw);
+  static_assert(sizeof(Ctl) <= kCtl, "barriers and tiles");
+  const uint32_t base = tc::smem_u32(raw) + kCtl;
   const uint32_t sq = base, kring = base + 2 * S::kTile, vring = kring + S::kKeyRing * S::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tt = a.tile_tokens, window = a.window;
@@ -357,6 +377,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::mbar_init(tc::smem_u32(&c.pfull[i][0]), 4);
       tc::mbar_init(tc::smem_u32(&c.pfull[i][1]), 4);
       tc::mbar_init(tc::smem_u32(&c.ofull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&c.oempty[i]), 4);
+      tc::mbar_init(tc::smem_u32(&c.lfull[i]), 4);
+      tc::mbar_init(tc::smem_u32(&c.lempty[i]), 4);
       tc::mbar_init(tc::smem_u32(&c.ifull[i]), 1);
       tc::mbar_init(tc::smem_u32(&c.iempty[i]), kItemReaders);
       tc::mbar_init(tc::smem_u32(&c.turn[i]), 1);
@@ -382,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto s_at = [&](int i) { return tmem + i * 128; };
   auto o_at = [&](int i) { return tmem + 256 + i * 128; };
 
-  if (warp >= kMmaWarp) {
+  if (warp >= kMmaWarp && warp < kEndWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
       const int per_slot = a.heads / a.pack;
@@ -514,6 +537,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           rv.next();
         }
         __syncwarp();
+        if (ok && it.bad_hi >= 0) {                    // rows that see a value that was zeroed
+          for (int x = 0; x < 2 * tt * a.pack; ++x) {
+            const int row = it.r0 + x / a.pack, at = row + p.off;
+            if (row >= it.lq || !sees_zeroed(it, at, window)) continue;
+            const int first = first_key(at, window);
+            redo_row(a, it.head + x % a.pack, it.q0 + row, (long long)it.k0 + first, at - first + 1, c.weight);
+          }
+        }
         if (ok && lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
       }
     } else if (lane == 0) {
@@ -531,7 +562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       Ring<S::kKeyRing> rk;
       Ring<S::kValRing> rv;
-      uint32_t np = 0, nq = 0, my = i ^ 1;                                 // parities of the phases to wait for
+      uint32_t np = 0, nq = 0, my = i ^ 1, no = 1;                         // parities of the phases to wait for
       bool ok = true;
       for (unsigned n = 0; ok; ++n) {
         ok = wait(c.ifull[n & 1], (n / 2) & 1);
@@ -555,6 +586,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint64_t vv = dv + rv.slot * kStep;
           if (pv && ok) {
             ok = wait(c.pfull[i][0], np);
+            if (j == first) {
+              ok = ok && wait(c.oempty[i], no);        // the item before is out of O
+              no ^= 1;
+            }
             tc::fence_after_sync();
             // the tiles take turns from here to the scores, so that one's products
             // run under the other's softmax
@@ -599,27 +634,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2;
     const uint32_t quad = (uint32_t)(warp & 3) * 32u << 16;
     const int in_tile = (warp & 3) * 32 + lane;             // the thread's row of the tile
-    const int quarter = lane & 3;
-    const int row_token = in_tile / a.pack, row_head = in_tile - row_token * a.pack;
+    const int row_token = in_tile / a.pack;
     const float sc = a.scale * kLog2e;
     const unsigned long long sc2 = pair(sc, sc);
-    unsigned ns = 0, no = 0;
+    unsigned ns = 0, nl = 0;
     bool ok = true;
     for (unsigned n = 0; ok; ++n) {
       ok = warp_wait(c, c.ifull[n & 1], (n / 2) & 1);
       if (!ok) break;
       const Item& it = c.item[n & 1];
       if (!it.live) break;
-      const int q0 = it.q0, k0 = it.k0, lq = it.lq;
       const Plan p = plan_of(it, tt, window);
       const Tile w = i ? p.t[1] : p.t[0];
-      const int row = w.r0 + row_token, head = it.head + row_head;
-      const int at = row + p.off;                           // the last key this row sees
+      const int at = w.r0 + row_token + p.off;                           // the last key this row sees
       float m = -INFINITY, l = 0.f;
       for (int j = w.first; j < w.last; ++j) {
         ok = warp_wait(c, c.sfull[i], ns & 1);
@@ -665,14 +697,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l *= f;
           if (j > w.first) {
 #pragma unroll 1
-            for (int x = 0; x < DP; x += 32) {
-              uint32_t o[32];
-              ld32(o_at(i) + quad + x, o);
+            for (int x = 0; x < DP; x += 16) {
+              uint32_t o[16];
+              ld16(o_at(i) + quad + x, o);
               ld_wait();
               tie(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              st32(o_at(i) + quad + x, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              st16(o_at(i) + quad + x, o);
             }
           }
         }
@@ -680,89 +712,116 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const unsigned long long mb2 = pair(-mb, -mb);
         unsigned long long sum[2] = {0ull, 0ull};                       // pairs of zeros
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t pw[32];
+        for (int x = 0; x < 4; ++x) {
+          uint32_t pw[16];
 #pragma unroll
-          for (int y = 0; y < 32; ++y) {
-            const uint32_t s0 = s[2 * x + y / 16][(2 * y) & 31], s1 = s[2 * x + y / 16][(2 * y + 1) & 31];
+          for (int y = 0; y < 16; ++y) {
             float p0, p1;
-            unpair(fma2(pair(__uint_as_float(s0), __uint_as_float(s1)), sc2, mb2), p0, p1);
+            unpair(fma2(pair(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])), sc2, mb2), p0, p1);
             p0 = ex2(p0), p1 = ex2(p1);
             sum[y & 1] = add2(sum[y & 1], pair(p0, p1));
             pw[y] = pack_bf16(p0, p1);
           }
-          st32(s_at(i) + quad + 32 * x, pw);
-          st_wait();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive(tc::smem_u32(&c.pfull[i][x]));
+          st16(s_at(i) + quad + 16 * x, pw);
+          if (x & 1) {
+            st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive(tc::smem_u32(&c.pfull[i][x >> 1]));
+          }
         }
         float a0, a1;
         unpair(add2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
       }
       if (ok && w.last > 0) {
-        ok = warp_wait(c, c.ofull[i], no & 1);
-        ++no;
+        ok = warp_wait(c, c.lempty[i], nl & 1 ^ 1);
+        ++nl;
+        c.sums[i][in_tile] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) arrive(tc::smem_u32(&c.lfull[i]));
       }
-      tc::fence_after_sync();
-      const bool mine = row < lq && row_token < tt;
-      const bool some = w.last > 0 && !(l == 0.f);
-      const float f = !ok ? NAN : some ? 1.f / l : 0.f;
-      // the rows of the quad: row quarter ^ y of it, null where there is none
-      __nv_bfloat16* to[4];
+      __syncwarp();
+      if (lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kEndRegs));
+    const uint32_t quad = (uint32_t)(warp & 3) * 32u << 16;
+    const int in_tile = (warp & 3) * 32 + lane, quarter = lane & 3;
+    const int row_token = in_tile / a.pack, row_head = in_tile - row_token * a.pack;
+    unsigned no[2] = {0, 0};
+    bool ok = true;
+    for (unsigned n = 0; ok; ++n) {
+      ok = warp_wait(c, c.ifull[n & 1], (n / 2) & 1);
+      if (!ok) break;
+      const Item& it = c.item[n & 1];
+      if (!it.live) break;
+      const Plan p = plan_of(it, tt, window);
+      const int head = it.head + row_head;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int rr = __shfl_xor_sync(kAll, row, y), hh = __shfl_xor_sync(kAll, head, y);
-        to[y] = __shfl_xor_sync(kAll, (int)mine, y) ? a.out + (long long)(q0 + rr) * a.out_token + hh * a.out_head : nullptr;
-      }
-#pragma unroll 1
-      for (int x = 0; x < DP; x += 32) {
-        uint32_t o[32];
+      for (int i = 0; i < 2; ++i) {
+        const Tile w = p.t[i];
+        const int row = w.r0 + row_token, at = row + p.off;
+        float m = -INFINITY, l = 0.f;
         if (w.last > 0) {
-          ld32(o_at(i) + quad + x, o);
-          ld_wait();
-          tie(o);
+          ok = ok && warp_wait(c, c.lfull[i], no[i] & 1) && warp_wait(c, c.ofull[i], no[i] & 1);
+          ++no[i];
+          const float2 v = c.sums[i][in_tile];
+          m = v.x, l = v.y;
+          __syncwarp();
+          if (lane == 0) arrive(tc::smem_u32(&c.lempty[i]));
         }
-        if (!some) {
+        tc::fence_after_sync();
+        const bool mine = row < it.lq && row_token < tt && !sees_zeroed(it, at, window);   // (those: redo_row)
+        const bool some = w.last > 0 && !(l == 0.f);
+        const float f = !ok ? NAN : some ? 1.f / l : 0.f;
+        // the rows of the quad: row quarter ^ y of it, null where there is none
+        __nv_bfloat16* to[4];
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = 0u;
+        for (int y = 0; y < 4; ++y) {
+          const int rr = __shfl_xor_sync(kAll, row, y), hh = __shfl_xor_sync(kAll, head, y);
+          to[y] = __shfl_xor_sync(kAll, (int)mine, y) ? a.out + (long long)(it.q0 + rr) * a.out_token + hh * a.out_head : nullptr;
         }
+#pragma unroll 1
+        for (int x = 0; x < DP; x += 32) {
+          uint32_t o[32];
+          if (w.last > 0) {
+            ld32(o_at(i) + quad + x, o);
+            ld_wait();
+            tie(o);
+          }
+          if (!some) {
 #pragma unroll
-        for (int y = 0; y < 16; ++y) o[y] = pack_bf16(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
-        // The four lanes of a quad exchange 16-byte pieces, so that each store writes 64
-        // bytes of eight rows instead of 16 bytes of 32: lane q of the quad gets piece q
-        // of every row of the quad, row q ^ y in piece y.
-        uint32_t v[4][4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const uint32_t low = quarter & 1 ? o[4 * (y ^ 1) + z] : o[4 * y + z];            // piece quarter ^ y, bit 0 settled
-            const uint32_t high = quarter & 1 ? o[4 * (y ^ 3) + z] : o[4 * (y ^ 2) + z];
-            v[y][z] = quarter & 2 ? high : low;
+            for (int y = 0; y < 32; ++y) o[y] = 0u;
           }
 #pragma unroll
-        for (int y = 1; y < 4; ++y)
+          for (int y = 0; y < 16; ++y) o[y] = pack_bf16(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+          // The four lanes of a quad exchange 16-byte pieces, so that each store writes 64
+          // bytes of eight rows instead of 16 bytes of 32: lane q of the quad gets piece q
+          // of every row of the quad, row q ^ y in piece y.
+          uint32_t v[4][4];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) v[y][z] = __shfl_xor_sync(kAll, v[y][z], y);
+          for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if (to[y] && x + 8 * quarter < a.D)
-            *reinterpret_cast<uint4*>(to[y] + x + 8 * quarter) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
-      }
-      tc::fence_before_sync();
-      if (mine && a.lse)
-        a.lse[(long long)(q0 + row) * a.heads + head] = !ok ? NAN : some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
-      // rows that see a value that was zeroed
-      const int from = window > 0 && at - window + 1 > 0 ? at - window + 1 : 0;
-      unsigned again = __ballot_sync(kAll, mine && ok && it.bad_hi >= from && it.bad_lo <= at);
-      while (again) {
-        const int b = __ffs(again) - 1;
-        again &= again - 1;
-        const int rr = __shfl_sync(kAll, row, b), hh = __shfl_sync(kAll, head, b), last = rr + p.off;
-        const int first = window > 0 && last - window + 1 > 0 ? last - window + 1 : 0;
-        redo_row(a, hh, q0 + rr, (long long)k0 + first, last - first + 1);
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t low = quarter & 1 ? o[4 * (y ^ 1) + z] : o[4 * y + z];            // piece quarter ^ y, bit 0 settled
+              const uint32_t high = quarter & 1 ? o[4 * (y ^ 3) + z] : o[4 * (y ^ 2) + z];
+              v[y][z] = quarter & 2 ? high : low;
+            }
+#pragma unroll
+          for (int y = 1; y < 4; ++y)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[y][z] = __shfl_xor_sync(kAll, v[y][z], y);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (to[y] && x + 8 * quarter < a.D)
+              *reinterpret_cast<uint4*>(to[y] + x + 8 * quarter) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (w.last > 0 && lane == 0) arrive(tc::smem_u32(&c.oempty[i]));
+        if (mine && a.lse)
+          a.lse[(long long)(it.q0 + row) * a.heads + head] = !ok ? NAN : some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
       }
       __syncwarp();
       if (lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
