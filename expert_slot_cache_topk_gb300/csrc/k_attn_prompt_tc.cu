@@ -79,11 +79,21 @@ struct PromptTc {
   float scale;
 };
 
-// One item, found by the load warp and read by all others
+// What a tile of 128 rows has to do: the steps [first, last) of 128 keys, from its
+// first query r0 on
+struct Tile {
+  int r0, first, last;
+};
+
+// One item, found by the load warp and read by all others: everything that they
+// would otherwise each work out in code that runs once per item, and so slowly
 struct Item {
   int live;                      // 0: no more items
   int q0, k0, lq, lk;            // the sequence's first query and key, and how many of each
-  int r0, head;                  // the first tile's first token; the first of its `pack` heads
+  int head;                      // the first of its `pack` heads
+  Tile t[2];
+  int off, first, last;          // last key of query r: r + off; steps of the item
+  int clean_from, clean_to;      // steps in [clean_from, clean_to) are crossed by no mask
   int bad_lo, bad_hi;            // keys (of the sequence) with a value that was zeroed: first, last
 };
 
@@ -240,37 +250,28 @@ struct Ring {
   }
 };
 
-// What a tile of 128 rows has to do: the steps [first, last) of 128 keys
-struct Tile {
-  int r0, first, last;
-};
-struct Plan {
-  Tile t[2];
-  int off, first, last;          // key of query r: r + off; steps of the item
-  int clean_from, clean_to;      // steps in [clean_from, clean_to) are crossed by no mask
-};
-__device__ __forceinline__ Plan plan_of(const Item& it, int tile_tokens, int window) {
-  Plan p;
-  p.off = it.lk - it.lq;
+// the item's tiles, from the first query r0 of the first one on
+__device__ __forceinline__ void plan(Item& it, int r0, int tile_tokens, int window) {
+  it.off = it.lk - it.lq;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    Tile& t = p.t[i];
-    t.r0 = it.r0 + i * tile_tokens;
-    const int end = (t.r0 + tile_tokens < it.lq ? t.r0 + tile_tokens : it.lq) + p.off;      // keys before `end` are seen
-    const int begin = window > 0 ? t.r0 + p.off - window + 1 : 0;
+    Tile& t = it.t[i];
+    t.r0 = r0 + i * tile_tokens;
+    const int end = (t.r0 + tile_tokens < it.lq ? t.r0 + tile_tokens : it.lq) + it.off;      // keys before `end` are seen
+    const int begin = window > 0 ? t.r0 + it.off - window + 1 : 0;
     t.first = begin > 0 ? begin / kKeys : 0;
     t.last = t.r0 < it.lq && end > 0 ? (end + kKeys - 1) / kKeys : 0;
     if (t.last <= t.first) t.first = t.last = 0;
   }
-  p.first = p.t[0].last > 0 ? p.t[0].first : p.t[1].first;
-  p.last = p.t[1].last > 0 ? p.t[1].last : p.t[0].last;
+  it.first = it.t[0].last > 0 ? it.t[0].first : it.t[1].first;
+  it.last = it.t[1].last > 0 ? it.t[1].last : it.t[0].last;
   // the diagonal of the first tile at work crosses first, the window of the last one leaves last
-  const int low = (p.t[0].last > 0 ? p.t[0].r0 : p.t[1].r0) + p.off;
-  const int high = (p.t[1].last > 0 ? p.t[1].r0 : p.t[0].r0) + tile_tokens - 1 + p.off - window;
-  p.clean_to = low >= 0 ? (low + 1) / kKeys : 0;
-  p.clean_from = window > 0 && high >= 0 ? high / kKeys + 1 : 0;
-  return p;
+  const int low = (it.t[0].last > 0 ? it.t[0].r0 : it.t[1].r0) + it.off;
+  const int high = (it.t[1].last > 0 ? it.t[1].r0 : it.t[0].r0) + tile_tokens - 1 + it.off - window;
+  it.clean_to = low >= 0 ? (low + 1) / kKeys : 0;
+  it.clean_from = window > 0 && high >= 0 ? high / kKeys + 1 : 0;
 }
+
 // One warp: values of keys past the sequence's end, and values that are not
 // finite, become zero in a tile of 128 keys; the item notes the latter's keys.
 template <int DP>
@@ -429,10 +430,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         auto clamp = [](int v, int x, int y) { return v < x ? x : v > y ? y : v; };
         const int s0 = a.starts_q[lo];
-        it.r0 = (slot - s0 / (2 * tt) - lo) * (2 * tt);
+        const int r0 = (slot - s0 / (2 * tt) - lo) * (2 * tt);
         it.q0 = clamp(s0, 0, a.q_tokens), it.lq = clamp(a.starts_q[lo + 1], it.q0, a.q_tokens) - it.q0;
         it.k0 = clamp(a.starts_k[lo], 0, a.k_tokens), it.lk = clamp(a.starts_k[lo + 1], it.k0, a.k_tokens) - it.k0;
-        if (it.r0 >= 0 && it.r0 < it.lq) {
+        if (r0 >= 0 && r0 < it.lq) {
+          plan(it, r0, tt, window);
           const int z = published & 1;
           if (published >= 2) ok = warp_wait(c, c.iempty[z], (published / 2 - 1) & 1);
           if (!ok) break;
@@ -441,27 +443,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             arrive(tc::smem_u32(&c.ifull[z]));
           }
           ++published;
-          const Plan p = plan_of(it, tt, window);
           if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (p.t[i].last == 0 || !ok) continue;
+            const int kh = it.head / a.group;
+            auto load_q = [&](int i) {
+              if (it.t[i].last == 0 || !ok) return;
               if (nq[i] > 0) ok = wait_for(c, c.qempty[i], (nq[i] - 1) & 1);
               ++nq[i];
-              if (!ok) continue;
+              if (!ok) return;
               const uint32_t bar = tc::smem_u32(&c.qfull[i]);
               arrive_tx(bar, tt * a.pack * DP * 2);
               for (int x = 0; x < DP / 64; ++x)
-                tma_3d(sq + i * S::kTile + x * S::kBox, &mq, 64 * x, it.head, it.q0 + p.t[i].r0, bar);
-            }
-            const int kh = it.head / a.group;
-            for (int j = p.first; j < p.last && ok; ++j) {
+                tma_3d(sq + i * S::kTile + x * S::kBox, &mq, 64 * x, it.head, it.q0 + it.t[i].r0, bar);
+            };
+            // in the order in which the item before lets go of the space
+            load_q(0);
+            for (int j = it.first; j < it.last && ok; ++j) {
               ok = wait_for(c, c.kempty[rk.slot], rk.turn ^ 1);        // a fresh slot's wait passes at once
               if (!ok) break;
               uint32_t bar = tc::smem_u32(&c.kfull[rk.slot]), dst = kring + rk.slot * S::kTile;
               arrive_tx(bar, S::kTile);
               for (int x = 0; x < DP / 64; ++x) tma_3d(dst + x * S::kBox, &mk, 64 * x, kh, it.k0 + j * kKeys, bar);
               rk.next();
+              if (j == it.first) load_q(1);
+              if (!ok) break;
               ok = wait_for(c, c.vempty[rv.slot], rv.turn ^ 1);
               if (!ok) break;
               bar = tc::smem_u32(&c.vfull[rv.slot]), dst = vring + rv.slot * S::kTile;
@@ -527,22 +531,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         Item& it = c.item[n & 1];
         if (!it.live) break;
-        const Plan p = plan_of(it, tt, window);
+        const int first = it.first, last = it.last, clean_from = it.clean_from, clean_to = it.clean_to;
         const int lk = it.lk;
-        for (int j = p.first; j < p.last; ++j) {
+        for (int j = first; j < last; ++j) {
           ok = warp_wait(c, c.vfull[rv.slot], rv.turn);
           if (!ok) break;
-          if (j < p.clean_from || j >= p.clean_to) clean<DP>(vring + rv.slot * S::kTile, lane, j * kKeys, lk, it);
+          if (j < clean_from || j >= clean_to) clean<DP>(vring + rv.slot * S::kTile, lane, j * kKeys, lk, it);
           if (lane == 0) arrive(tc::smem_u32(&c.vready[rv.slot]));
           rv.next();
         }
         __syncwarp();
         if (ok && it.bad_hi >= 0) {                    // rows that see a value that was zeroed
           for (int x = 0; x < 2 * tt * a.pack; ++x) {
-            const int row = it.r0 + x / a.pack, at = row + p.off;
+            const int row = it.t[0].r0 + x / a.pack, at = row + it.off;
             if (row >= it.lq || !sees_zeroed(it, at, window)) continue;
-            const int first = first_key(at, window);
-            redo_row(a, it.head + x % a.pack, it.q0 + row, (long long)it.k0 + first, at - first + 1, c.weight);
+            const int from = first_key(at, window);
+            redo_row(a, it.head + x % a.pack, it.q0 + row, (long long)it.k0 + from, at - from + 1, c.weight);
           }
         }
         if (ok && lane == 0) arrive(tc::smem_u32(&c.iempty[n & 1]));
@@ -567,20 +571,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (unsigned n = 0; ok; ++n) {
         ok = wait(c.ifull[n & 1], (n / 2) & 1);
         if (!ok) break;
-        const Item it = c.item[n & 1];
+        const Item& it = c.item[n & 1];
+        const int live = it.live, first = it.t[i].first, last = it.t[i].last, begin = it.first, end = it.last;
         arrive(tc::smem_u32(&c.iempty[n & 1]));
-        if (!it.live) break;
-        const Plan p = plan_of(it, tt, window);
-        const int first = i ? p.t[1].first : p.t[0].first, last = i ? p.t[1].last : p.t[0].last;
+        if (!live) break;
         if (last > 0) {
           ok = wait(c.qfull[i], nq);
           nq ^= 1;
         }
         // S(first .. last - 1) and PV in turn; the other steps' tiles are only passed on
-        for (int j = p.first - 1; j < p.last && ok; ++j) {
+        for (int j = begin - 1; j < end && ok; ++j) {
           const bool pv = j >= first && j < last, sc = j + 1 >= first && j + 1 < last;
-          if (j >= p.first) ok = wait(c.vready[rv.slot], rv.turn) && wait(c.vfull[rv.slot], rv.turn);
-          if (j + 1 < p.last && ok) ok = wait(c.kfull[rk.slot], rk.turn);
+          if (j >= begin) ok = wait(c.vready[rv.slot], rv.turn) && wait(c.vfull[rv.slot], rv.turn);
+          if (j + 1 < end && ok) ok = wait(c.kfull[rk.slot], rk.turn);
           // the weights come in two halves: the first 64 keys' product runs while
           // the softmax works on the others
           const uint64_t vv = dv + rv.slot * kStep;
@@ -603,8 +606,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tc::fence_after_sync();
             }
           }
-          if (ok && !pv) ok = wait(c.turn[i], my);
-          my ^= 1;
+          if (j >= begin) {
+            if (ok && !pv) ok = wait(c.turn[i], my);
+            my ^= 1;
+          }
           if (!ok) break;
           if (pv) {
 #pragma unroll
@@ -619,14 +624,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             tc::mma_commit(tc::smem_u32(&c.sfull[i]));
           }
-          arrive(tc::smem_u32(&c.turn[i ^ 1]));
+          if (j >= begin) arrive(tc::smem_u32(&c.turn[i ^ 1]));
           if (j + 2 == last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
           if (j + 1 == last && last > 0) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
-          if (j + 1 < p.last) {
+          if (j + 1 < end) {
             tc::mma_commit(tc::smem_u32(&c.kempty[rk.slot]));
             rk.next();
           }
-          if (j >= p.first) {
+          if (j >= begin) {
             tc::mma_commit(tc::smem_u32(&c.vempty[rv.slot]));
             rv.next();
           }
@@ -649,9 +654,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) break;
       const Item& it = c.item[n & 1];
       if (!it.live) break;
-      const Plan p = plan_of(it, tt, window);
-      const Tile w = i ? p.t[1] : p.t[0];
-      const int at = w.r0 + row_token + p.off;                           // the last key this row sees
+      const Tile w = it.t[i];
+      const int clean_from = it.clean_from, clean_to = it.clean_to;
+      const int at = w.r0 + row_token + it.off;                           // the last key this row sees
       float m = -INFINITY, l = 0.f;
       for (int j = w.first; j < w.last; ++j) {
         ok = warp_wait(c, c.sfull[i], ns & 1);
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) tie(s[x]);
         const int key = j * kKeys;
-        if (j < p.clean_from || j >= p.clean_to) {
+        if (j < clean_from || j >= clean_to) {
           const int hi = at - key, lo = window > 0 ? hi - window : -1;   // seen: lo < position <= hi
           // the last row's and the first row's bounds: 32 keys that all rows of the warp
           // see need no look at single ones
@@ -749,23 +754,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t quad = (uint32_t)(warp & 3) * 32u << 16;
     const int in_tile = (warp & 3) * 32 + lane, quarter = lane & 3;
     const int row_token = in_tile / a.pack, row_head = in_tile - row_token * a.pack;
-    unsigned no[2] = {0, 0};
+    unsigned no = 0;                                        // bit i: parity of tile i's next phases
     bool ok = true;
     for (unsigned n = 0; ok; ++n) {
       ok = warp_wait(c, c.ifull[n & 1], (n / 2) & 1);
       if (!ok) break;
       const Item& it = c.item[n & 1];
       if (!it.live) break;
-      const Plan p = plan_of(it, tt, window);
       const int head = it.head + row_head;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        const Tile w = p.t[i];
-        const int row = w.r0 + row_token, at = row + p.off;
+        const Tile w = it.t[i];
+        const int row = w.r0 + row_token, at = row + it.off;
         float m = -INFINITY, l = 0.f;
         if (w.last > 0) {
-          ok = ok && warp_wait(c, c.lfull[i], no[i] & 1) && warp_wait(c, c.ofull[i], no[i] & 1);
-          ++no[i];
+          ok = ok && warp_wait(c, c.lfull[i], no >> i & 1) && warp_wait(c, c.ofull[i], no >> i & 1);
+          no ^= 1u << i;
           const float2 v = c.sums[i][in_tile];
           m = v.x, l = v.y;
           __syncwarp();
