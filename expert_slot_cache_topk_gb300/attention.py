@@ -21,6 +21,9 @@ _DTYPE = {torch.bfloat16: _abi.MOE_BF16, torch.float32: _abi.MOE_F32}
 _byref = C.byref
 
 
+# The checks run at every call, next to kernels of a few microseconds: they read
+# each attribute once and build their messages only when they refuse.
+
 def _hidden_type(t: torch.Tensor) -> int:
     code = _DTYPE.get(t.dtype)
     if code is None:
@@ -28,36 +31,59 @@ def _hidden_type(t: torch.Tensor) -> int:
     return code
 
 
-def _like(t: Optional[torch.Tensor], ref: torch.Tensor, what: str):
-    """t has ref's type and device."""
-    if t is not None and (t.dtype != ref.dtype or t.device != ref.device):
-        raise TypeError(f"{what} must be a {ref.dtype} tensor on {ref.device}, got {t.dtype} on {t.device}")
+def _wrong_kind(t, ref, what):
+    raise TypeError(f"{what} must be a {ref.dtype} tensor on {ref.device}, got {t.dtype} on {t.device}")
 
 
-def _ints(t: torch.Tensor, n: Optional[int], device, what: str) -> int:
+def _rows(t, x, dtype, device, shape, what):
+    """(address, row distance) of a tensor with x's type, place and shape and contiguous rows."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _wrong_kind(t, x, what)
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.data_ptr(), row
+
+
+def _vector(t, x, dtype, device, n, what):
+    """Address of a contiguous vector of n entries with x's type and place."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _wrong_kind(t, x, what)
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride()[0] != 1):
+        raise ValueError(f"{what} must be a contiguous vector of {n} entries")
+    return t.data_ptr()
+
+
+def _ints(t: torch.Tensor, n: Optional[int], device: int, what: str) -> int:
     """Address of a contiguous int32 vector of n entries."""
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise TypeError(f"{what} must be an int32 vector" + ("" if n is None else f" of {n} entries") + f" on {device}")
-    if t.shape[0] > 1 and t.stride(0) != 1:
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise TypeError(f"{what} must be an int32 vector" + ("" if n is None else f" of {n} entries")
+                        + f" on device {device}")
+    if t.stride()[0] != 1 and t.shape[0] > 1:
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, shape, what: str):
-    """(address, token distance, head distance) of a [tokens, heads, head_dim] tensor."""
-    if tuple(t.shape) != shape:
+def _heads(t, ref, dtype, device, shape, what: str):
+    """(address, token distance, head distance) of a [tokens, heads, head_dim] tensor of ref's type and place."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _wrong_kind(t, ref, what)
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
-    st, sh, sd = t.stride()
-    if sd != 1 and shape[2] != 1:
+    token, head, dim = t.stride()
+    if dim != 1 and shape[2] != 1:
         raise ValueError(f"{what}: the head dimension must be contiguous")
-    return t.data_ptr(), st, sh
+    return t.data_ptr(), token, head
 
 
-def _lse(lse: Optional[torch.Tensor], n: int, heads: int, device) -> Optional[int]:
+def _lse(lse: Optional[torch.Tensor], n: int, heads: int, device: int) -> Optional[int]:
     if lse is None:
         return None
-    if lse.dtype != torch.float32 or lse.device != device or tuple(lse.shape) != (n, heads) or not lse.is_contiguous():
-        raise TypeError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on {device}")
+    if lse.dtype is not torch.float32 or lse.get_device() != device or lse.shape != (n, heads) or \
+            not lse.is_contiguous():
+        raise TypeError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on device {device}")
     return lse.data_ptr()
 
 
@@ -74,38 +100,40 @@ def norm_residual(x, block=None, pre_weight=None, x_out=None, y=None, post_weigh
     token), [1, hidden] or [hidden] (one per channel), or [tokens, hidden].
     """
     code = _hidden_type(x)
-    if x.dim() != 2:
+    dtype, device, shape = x.dtype, x.get_device(), x.shape
+    if len(shape) != 2:
         raise ValueError("x must have shape [tokens, hidden]")
-    T, H = x.shape
-    rows = []
-    for t, what in ((x, "x"), (block, "block"), (x_out, "x_out"), (y, "y")):
-        if t is None:
-            rows.append((None, 0))
-            continue
-        if t.dtype != x.dtype or t.device != x.device:
-            raise TypeError(f"{what} must be a {x.dtype} tensor on {x.device}")
-        if t.shape != x.shape or (H > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what} must have shape {[T, H]} and contiguous rows")
-        rows.append((t.data_ptr(), t.stride(0)))
-    for t, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
-        _like(t, x, what)
-        if t is not None and (t.shape != (H,) or (H > 1 and t.stride(0) != 1)):
-            raise ValueError(f"{what} must be a contiguous vector of {H} entries")
-    g, g_row, g_col = None, 0, 0
+    T, H = shape
+    xp, x_row = _rows(x, x, dtype, device, shape, "x")
+    b = xo = yo = pw = w = g = None
+    b_row = xo_row = yo_row = g_row = g_col = 0
+    if block is not None:
+        b, b_row = _rows(block, x, dtype, device, shape, "block")
+    if x_out is not None:
+        xo, xo_row = _rows(x_out, x, dtype, device, shape, "x_out")
+    if y is not None:
+        yo, yo_row = _rows(y, x, dtype, device, shape, "y")
+    if post_weight is not None:
+        pw = _vector(post_weight, x, dtype, device, H, "post_weight")
+    if pre_weight is not None:
+        w = _vector(pre_weight, x, dtype, device, H, "pre_weight")
     if gate is not None:
-        _like(gate, x, "gate")
-        if gate.dim() == 1:
-            gate = gate[None]
-        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
+        if gate.dtype is not dtype or gate.get_device() != device:
+            _wrong_kind(gate, x, "gate")
+        gs = gate.shape
+        if len(gs) == 1:
+            gate, gs = gate[None], (1, gs[0])
+        if len(gs) != 2 or gs[0] not in (1, T) or gs[1] not in (1, H):
             raise ValueError(f"gate must broadcast to {[T, H]}")
-        g_col = int(gate.shape[1] > 1)
-        if g_col and gate.stride(1) != 1:
-            raise ValueError("gate rows must be contiguous")
-        g, g_row = gate.data_ptr(), gate.stride(0) if gate.shape[0] > 1 else 0
-    a = _abi.moe_norm_args(code, H, T, rows[0][0], rows[1][0],
-                           None if post_weight is None else post_weight.data_ptr(), g,
-                           None if pre_weight is None else pre_weight.data_ptr(), rows[2][0], rows[3][0],
-                           rows[0][1], rows[1][1], g_row, rows[2][1], rows[3][1], g_col, res_scale, eps)
+        g_row, col = gate.stride()
+        if gs[0] == 1:
+            g_row = 0
+        if gs[1] > 1:
+            g_col = 1
+            if col != 1:
+                raise ValueError("gate rows must be contiguous")
+        g = gate.data_ptr()
+    a = _abi.moe_norm_args(code, H, T, xp, b, pw, g, w, xo, yo, x_row, b_row, g_row, xo_row, yo_row, g_col, res_scale, eps)
     _abi._check(_abi.lib().moe_norm_residual(_byref(a), _abi._stream(stream)))
 
 
@@ -122,22 +150,21 @@ def attn_prompt(q, k, v, starts_q, starts_k, out, scale=None, window=0, lse=None
     nothing gives zeros and lse = -inf.
     """
     code = _hidden_type(q)
-    if q.dim() != 3 or k.dim() != 3:
+    dtype, device, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3:
         raise ValueError("q, k and v must have shape [tokens, heads, head_dim]")
-    Tq, Hq, D = q.shape
-    Tk, Hkv = k.shape[0], k.shape[1]
-    for t, what in ((k, "k"), (v, "v"), (out, "out")):
-        _like(t, q, what)
-    qp, q_token, q_head = _heads(q, (Tq, Hq, D), "q")
-    kp, k_token, k_head = _heads(k, (Tk, Hkv, D), "k")
-    vp, v_token, v_head = _heads(v, (Tk, Hkv, D), "v")
-    op, o_token, o_head = _heads(out, (Tq, Hq, D), "out")
+    Tq, Hq, D = qs
+    Tk, Hkv, _ = ks
+    qp, q_token, q_head = _heads(q, q, dtype, device, qs, "q")
+    kp, k_token, k_head = _heads(k, q, dtype, device, (Tk, Hkv, D), "k")
+    vp, v_token, v_head = _heads(v, q, dtype, device, ks, "v")
+    op, o_token, o_head = _heads(out, q, dtype, device, qs, "out")
     n = starts_q.shape[0] - 1 if starts_q.dim() else -1
     if n < 0:
         raise ValueError("starts_q and starts_k need at least one entry")
-    a = _abi.moe_prompt_args(code, Hq, Hkv, D, n, Tq, Tk, _ints(starts_q, n + 1, q.device, "starts_q"),
-                             _ints(starts_k, n + 1, q.device, "starts_k"), qp, kp, vp, op,
-                             _lse(lse, Tq, Hq, q.device), q_token, q_head, k_token, k_head, v_token, v_head,
+    a = _abi.moe_prompt_args(code, Hq, Hkv, D, n, Tq, Tk, _ints(starts_q, n + 1, device, "starts_q"),
+                             _ints(starts_k, n + 1, device, "starts_k"), qp, kp, vp, op,
+                             _lse(lse, Tq, Hq, device), q_token, q_head, k_token, k_head, v_token, v_head,
                              o_token, o_head, D ** -0.5 if scale is None else scale, window)
     _abi._check(_abi.lib().moe_attn_prompt(_byref(a), _abi._stream(stream)))
 
@@ -158,7 +185,8 @@ class KVPages:
 
     def __init__(self, k, v, table, lens, refs, max_heads: Optional[int] = None):
         code = _hidden_type(k)
-        _like(v, k, "v")
+        if v.dtype is not k.dtype or v.device != k.device:
+            _wrong_kind(v, k, "v")
         if k.dim() != 5 or v.shape != k.shape or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("k and v must be contiguous [layers, num_pages, kv_heads, page_tokens, head_dim]")
         if not k.is_cuda:
@@ -169,11 +197,12 @@ class KVPages:
         seqs, columns = table.shape
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
         self.device = k.device
+        self._dev, self._dtype = k.get_device(), k.dtype
         self.kv_heads, self.head_dim, self.max_seqs, self.num_pages = kv_heads, dim, seqs, pages
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._kv = _abi.moe_kv_pages(code, layers, kv_heads, dim, page, pages, seqs, columns, k.data_ptr(), v.data_ptr(),
-                                     table.data_ptr(), _ints(lens, seqs, k.device, "lens"),
-                                     _ints(refs, pages, k.device, "refs"), self.status.data_ptr(), None, 0)
+                                     table.data_ptr(), _ints(lens, seqs, self._dev, "lens"),
+                                     _ints(refs, pages, self._dev, "refs"), self.status.data_ptr(), None, 0)
         self.max_heads = 64 * kv_heads if max_heads is None else max_heads
         need = C.c_size_t()
         _abi._check(_abi.lib().moe_kv_work_bytes(_byref(self._kv), self.max_heads, _byref(need)))
@@ -193,7 +222,7 @@ class KVPages:
                    torch.zeros(num_pages, **ints), max_heads)
 
     def _list(self, t, what, n=None) -> int:
-        return _ints(t, n, self.device, what)
+        return _ints(t, n, self._dev, what)
 
     def reserve(self, seqs, counts, stream=None):
         """Room for counts[i] more tokens in sequence seqs[i] (distinct rows).  New pages are the lowest free
@@ -206,11 +235,9 @@ class KVPages:
         """Write one layer's keys and values of the newest tokens: rows starts[i] : starts[i + 1] of k and v
         [tokens, kv_heads, head_dim] are the last tokens of sequence seqs[i] (room was reserved for them)."""
         n, T = seqs.shape[0], k.shape[0]
-        _like(k, self.k, "k")
-        _like(v, self.k, "v")
         shape = (T, self.kv_heads, self.head_dim)
-        kp, kt, kh = _heads(k, shape, "k")
-        vp, vt, vh = _heads(v, shape, "v")
+        kp, kt, kh = _heads(k, self.k, self._dtype, self._dev, shape, "k")
+        vp, vt, vh = _heads(v, self.k, self._dtype, self._dev, shape, "v")
         _abi._check(_abi.lib().moe_kv_append(self._ref, layer, self._list(seqs, "seqs"),
                                              self._list(starts, "starts", n + 1), n, kp, kt, kh, vp, vt, vh, T,
                                              _abi._stream(stream)))
@@ -256,17 +283,15 @@ class KVPages:
         """Attention of one new token per sequence: q, out [n, heads, head_dim]; row i reads sequence seqs[i]
         (rows may repeat), its last `window` tokens if window > 0.  scale defaults to head_dim ** -0.5.
         lse: float32 [n, heads] or None.  A sequence without tokens gives zeros and lse = -inf."""
-        _like(q, self.k, "q")
-        _like(out, self.k, "out")
         if q.dim() != 3:
             raise ValueError("q must have shape [n, heads, head_dim]")
-        n, heads = q.shape[0], q.shape[1]
+        n, heads, _ = q.shape
         shape = (n, heads, self.head_dim)
-        qp, qt, qh = _heads(q, shape, "q")
-        op, ot, oh = _heads(out, shape, "out")
+        qp, qt, qh = _heads(q, self.k, self._dtype, self._dev, shape, "q")
+        op, ot, oh = _heads(out, self.k, self._dtype, self._dev, shape, "out")
         _abi._check(_abi.lib().moe_attn_decode(self._ref, layer, qp, qt, qh, self._list(seqs, "seqs", n), n, heads,
                                                self.head_dim ** -0.5 if scale is None else scale, window, op, ot, oh,
-                                               _lse(lse, n, heads, self.device), _abi._stream(stream)))
+                                               _lse(lse, n, heads, self._dev), _abi._stream(stream)))
 
     def check(self, stream=None):
         """Synchronise the stream; raise MoeError (MOE_ESTATE) if a call was refused on the device since the
