@@ -1,0 +1,112 @@
+"""A small mixture-of-experts decoder served end to end: packed prompts, then one
+token per sequence and step.
+
+Every layer is norm -> attention -> norm -> experts.  The experts run through the
+expert-slot cache (``MoECache``), attention over whole prompts through
+``attn_prompt``, attention of new tokens over the paged key-value cache
+(``KVPages``), and the joins between the halves through ``norm_residual``.  The
+projections are plain matrix products.
+
+    python examples/decoder.py            # needs a GB300 and the built library
+"""
+
+import os
+import sys
+
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+if ROOT not in sys.path:
+    sys.path.insert(0, ROOT)
+
+from expert_slot_cache_topk_gb300 import _abi, synth  # noqa: E402
+from expert_slot_cache_topk_gb300.attention import KVPages, attn_prompt, norm_residual  # noqa: E402
+
+
+class Decoder:
+    """Random weights; f32 (exact to compare) or bf16."""
+
+    def __init__(self, layers=2, heads=4, kv_heads=2, head_dim=16, vocab=97, dtype=torch.float32, max_tokens=256,
+                 max_seqs=8, page_tokens=16, seed=0):
+        w = synth.WORKLOADS["tiny"].with_(layers=layers, wdtype="f32" if dtype == torch.float32 else "bf16")
+        H = w.hidden
+        self.dtype, self.layers, self.H, self.E = dtype, layers, H, w.experts
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.moe = _abi.MoECache(layers, w.experts, w.top_k, H, w.inter, w.wdtype, w.slots, max_tokens)
+        stride = self.moe.info()["slot_stride"]
+        for layer in range(layers):
+            synth.fill_layer_blocks(w, layer, self.moe.backing_view(layer).reshape(-1), stride)
+        g = torch.Generator().manual_seed(seed)
+        rand = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(dtype).cuda()  # noqa: E731
+        wide = (heads + 2 * kv_heads) * head_dim
+        self.embed = rand(vocab, H)
+        self.wqkv = [rand(H, wide, std=H ** -0.5) for _ in range(layers)]
+        self.wo = [rand(heads * head_dim, H, std=(heads * head_dim) ** -0.5) for _ in range(layers)]
+        self.router = [rand(H, w.experts, std=H ** -0.5) for _ in range(layers)]
+        self.norms = [1 + rand(H, std=0.1) for _ in range(2 * layers + 1)]     # before each half, and at the end
+        self.post = [1 + rand(H, std=0.1) for _ in range(layers)]              # after attention
+        max_pages = -(-512 // page_tokens)
+        self.kv = KVPages.empty(layers, kv_heads, head_dim, page_tokens, max_seqs * max_pages, max_seqs, max_pages,
+                                dtype=dtype, max_heads=heads)
+
+    def close(self):
+        self.moe.close()
+
+    def _forward(self, tokens, seqs, counts, prompt):
+        """Runs `tokens` (counts[i] of sequence seqs[i]); logits of every token."""
+        T = tokens.shape[0]
+        starts = torch.zeros(counts.shape[0] + 1, dtype=torch.int32, device="cuda")
+        starts[1:] = counts.cumsum(0)
+        self.kv.reserve(seqs, counts)
+        x = self.embed[tokens].clone()
+        h, m = torch.empty_like(x), torch.empty_like(x)
+        o = torch.empty(T, self.heads, self.head_dim, dtype=self.dtype, device="cuda")
+        norm_residual(x, pre_weight=self.norms[0], y=h)
+        for layer in range(self.layers):
+            qkv = (h @ self.wqkv[layer]).unflatten(1, (-1, self.head_dim))
+            q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
+            self.kv.append(layer, seqs, starts, k, v)
+            if prompt:
+                attn_prompt(q, k, v, starts, starts, o)
+            else:
+                self.kv.attend(layer, q, seqs, o)
+            a = o.flatten(1) @ self.wo[layer]
+            norm_residual(x, a, self.norms[2 * layer + 1], x, h, post_weight=self.post[layer], res_scale=0.5)
+            self.moe.forward(layer, h, (h @ self.router[layer]).float(), T, m)
+            norm_residual(x, m, self.norms[2 * layer + 2], x, h)
+        return h.float() @ self.embed.float().T
+
+    def prompt(self, prompts, seqs):
+        """Whole prompts (lists of token ids) into the empty sequences `seqs`; logits after each one's last token."""
+        lens = [len(p) for p in prompts]
+        tokens = torch.tensor([t for p in prompts for t in p], device="cuda")
+        counts = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        logits = self._forward(tokens, torch.tensor(seqs, dtype=torch.int32, device="cuda"), counts, True)
+        return logits[counts.cumsum(0) - 1]
+
+    def step(self, tokens, seqs):
+        """One more token for each sequence; its logits."""
+        seqs = torch.tensor(seqs, dtype=torch.int32, device="cuda")
+        return self._forward(torch.as_tensor(tokens, device="cuda"), seqs, torch.ones_like(seqs), False)
+
+
+def main():
+    d = Decoder()
+    prompts = [[5, 17, 3, 88, 41], [9] * 23, [1, 2, 3]]
+    logits = d.prompt(prompts, [0, 1, 2])
+    text = [list(p) for p in prompts]
+    for _ in range(20):
+        best = logits.argmax(1)
+        for t, b in zip(text, best.tolist()):
+            t.append(b)
+        logits = d.step(best, [0, 1, 2])
+    # what the decode steps say is what a fresh pass over the whole texts says
+    again = d.prompt(text, [3, 4, 5])
+    d.kv.check()
+    print("continuations", [t[len(p):] for t, p in zip(text, prompts)])
+    print("largest difference between decoding and one pass:", float((logits - again).abs().max()))
+    d.close()
+
+
+if __name__ == "__main__":
+    main()

@@ -433,6 +433,41 @@ def test_decode_extreme_scores(A, dtype, heads):
     assert torch.isfinite(out[1, heads // 2:]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_many_rows(A, dtype):
+    """More rows than a block of threads has threads, over sequences that repeat; some without tokens."""
+    lens = [0, 1, 16, 17, 40, 3, 0, 129]
+    kv, keys, values, g = fill(A, lens, dtype, 2, 64, 16, 21)
+    order = torch.randint(0, len(lens), (901,), generator=g).tolist()
+    q = randn(g, len(order), 4, 64, dtype=dtype)
+    out, lse = torch.full_like(q, 7.0), torch.full((len(order), 4), 7.0, device="cuda")
+    kv.attend(1, q, ints(order), out, lse=lse)
+    kv.check()
+    for i in range(0, len(order), 9):
+        s = order[i]
+        ro, rl = attn_ref(q[i:i + 1], keys[s], values[s], 0.125)
+        assert_attn(out[i:i + 1], lse[i:i + 1], ro, rl, float(values[s].double().abs().max()) if lens[s] else 0.0, f"row {i}")
+    empty = torch.tensor([lens[s] == 0 for s in order])
+    assert not out[empty].any() and torch.isneginf(lse[empty]).all() and torch.isfinite(lse[~empty]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30])
+def test_any_finite_scale(A, dtype, scale):
+    kv, keys, values, g = fill(A, [50, 3], dtype, 2, 64, 16, 22)
+    q = randn(g, 2, 4, 64, dtype=dtype)
+    out = torch.empty_like(q)
+    kv.attend(1, q, ints([0, 1]), out, scale=scale)
+    for i in range(2):
+        ro, _ = attn_ref(q[i:i + 1], keys[i], values[i], scale)
+        assert_attn(out[i:i + 1], None, ro, None, float(values[i].double().abs().max()), "decode")
+    lens = [(70, 90), (5, 5)]
+    q, k, v, sq, sk = prompt_inputs(g, lens, 4, 2, 64, dtype)
+    out = torch.empty_like(q)
+    A.attn_prompt(q, k, v, sq, sk, out, scale=scale)
+    check_prompt(q, k, v, lens, out, None, scale, 0)
+
+
 def test_decode_bad_rows_and_pages_give_zeros(A):
     from expert_slot_cache_topk_gb300._abi import MoeError
     kv, keys, values, g = fill(A, [100, 60], BF, 2, 64, 16, 6)
