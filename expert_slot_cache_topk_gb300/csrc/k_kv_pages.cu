@@ -59,6 +59,21 @@ Kv make(const moe_kv_pages& m) {
   return d;
 }
 
+// Two kernels of one call: the second is launched while the first runs (its blocks
+// are there when the first one ends) and waits for all of it before it reads.
+__device__ __forceinline__ void first_of_two() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void second_of_two() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_second(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 __device__ __forceinline__ void set_status(int32_t* status, int code) { atomicCAS(status, MOE_KV_OK, code); }
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
@@ -97,6 +112,7 @@ __global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int3
                                                           const int32_t* __restrict__ counts, int n) {
   __shared__ int bad, ncopy;
   const int t = threadIdx.x;
+  first_of_two();
   if (t == 0) bad = 0, ncopy = 0, d.hdr[H_COPIES] = 0;
   __syncthreads();
   for (int i = t; i < n; i += kBookThreads) {
@@ -215,6 +231,7 @@ __device__ __forceinline__ void copy_units(const char* __restrict__ src, char* _
 
 // Private copies of shared last pages: the tokens held, every layer, K and V
 __global__ void __launch_bounds__(256) k_copy_tails(const Kv d) {
+  second_of_two();
   const int copies = d.hdr[H_COPIES];
   const long long head_bytes = d.token_bytes << d.page_shift;
   const long long page_bytes = head_bytes * d.kv_heads;
@@ -231,11 +248,9 @@ __global__ void __launch_bounds__(256) k_copy_tails(const Kv d) {
   }
 }
 
-// Whole pages from list_src[i] to list_dst[i], i < n (n on the device when n_d is given)
-__global__ void __launch_bounds__(256) k_copy_pages(const Kv d, const int32_t* __restrict__ src,
-                                                    const int32_t* __restrict__ dst, int n,
-                                                    const int32_t* __restrict__ n_d) {
-  if (n_d) n = *n_d;
+// Whole pages from src[i] to dst[i], i < n, in every layer
+__device__ __forceinline__ void copy_pages(const Kv& d, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+                                           int n) {
   const long long page_bytes = (d.token_bytes << d.page_shift) * d.kv_heads;
   const long long part = page_bytes < 65536 ? page_bytes : 65536;   // bytes of one item
   const int parts = (int)((page_bytes + part - 1) / part);
@@ -255,6 +270,10 @@ __global__ void __launch_bounds__(256) k_copy_pages(const Kv d, const int32_t* _
     copy_units<uint4>(pool + from * page_bytes, pool + to * page_bytes, left < part ? left : part, threadIdx.x,
                       blockDim.x);
   }
+}
+__global__ void __launch_bounds__(256) k_copy_pages(const Kv d, const int32_t* __restrict__ src,
+                                                    const int32_t* __restrict__ dst, int n) {
+  copy_pages(d, src, dst, n);
 }
 
 // A list of rows is in range and has no row twice.  Each block decides for
@@ -312,6 +331,7 @@ __global__ void __launch_bounds__(256) k_truncate(const Kv d, const int32_t* __r
 // Fork, first launch: the sources' rows as they are, and one more reference each
 __global__ void __launch_bounds__(256) k_fork_read(const Kv d, const int32_t* __restrict__ src,
                                                    const int32_t* __restrict__ dst, int n) {
+  first_of_two();
   extern __shared__ unsigned bits[];
   const int bad = check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true);
   if (bad) {
@@ -335,7 +355,9 @@ __global__ void __launch_bounds__(256) k_fork_read(const Kv d, const int32_t* __
 __global__ void __launch_bounds__(256) k_fork_write(const Kv d, const int32_t* __restrict__ src,
                                                     const int32_t* __restrict__ dst, int n) {
   extern __shared__ unsigned bits[];
-  if (check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true)) return;
+  const int bad = check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true);
+  second_of_two();                       // refused or not: this kernel's end is the call's end
+  if (bad) return;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int s = dst[i], held = d.lens[s], now = d.mark[i];
     int old = pages_of(held, d.page_shift), cols = pages_of(now, d.page_shift);
@@ -399,24 +421,42 @@ __global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, 
 }
 
 // Compaction, first launch (one block): U, the movers (list_a) and the holes
-// (list_b) in ascending order, the reference counts afterwards.
+// (list_b) in ascending order, the reference counts afterwards.  Eight pages to a
+// thread and round: a pool of 8192 pages is one round of each scan.
 __global__ void __launch_bounds__(kBookThreads) k_compact_plan(const Kv d, int32_t* refs_out, int32_t* used_out) {
+  constexpr int kEach = 8, kRound = kEach * kBookThreads;
   const int t = threadIdx.x;
+  first_of_two();
   int used = 0;
-  for (int p0 = 0; p0 < d.num_pages; p0 += kBookThreads) {
-    const int p = p0 + t;
-    used += __syncthreads_count(p < d.num_pages && d.refs[p] > 0);
+  for (int p0 = 0; p0 < d.num_pages; p0 += kRound) {
+    int mine = 0, total;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int p = p0 + kEach * t + j;
+      mine += p < d.num_pages && d.refs[p] > 0;
+    }
+    block_scan(mine, &total);
+    used += total;
   }
   int movers = 0, holes = 0;
-  for (int p0 = 0; p0 < d.num_pages; p0 += kBookThreads) {
-    const int p = p0 + t;
-    const bool in = p < d.num_pages;
-    const bool busy = in && d.refs[p] > 0;
-    const int m = busy && p >= used, h = in && !busy && p < used;
+  for (int p0 = 0; p0 < d.num_pages; p0 += kRound) {
+    unsigned m = 0, h = 0;                                   // bit j: page j of the thread's moves, or is a hole
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int p = p0 + kEach * t + j;
+      const bool in = p < d.num_pages, busy = in && d.refs[p] > 0;
+      m |= (unsigned)(busy && p >= used) << j;
+      h |= (unsigned)(in && !busy && p < used) << j;
+    }
     int total;
-    const int at = block_scan(m | h << 16, &total);
-    if (m) d.list_a[movers + (at & 0xffff)] = p;
-    if (h) d.list_b[holes + (at >> 16)] = p;
+    int at = block_scan(__popc(m) | __popc(h) << 16, &total);
+    int am = movers + (at & 0xffff), ah = holes + (at >> 16);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int p = p0 + kEach * t + j;
+      if (m >> j & 1u) d.list_a[am++] = p;
+      if (h >> j & 1u) d.list_b[ah++] = p;
+    }
     movers += total & 0xffff, holes += total >> 16;
   }
   __syncthreads();
@@ -433,9 +473,10 @@ __global__ void __launch_bounds__(kBookThreads) k_compact_plan(const Kv d, int32
   }
 }
 
-// Compaction, last launch: every table entry that names a mover names its hole
-// (the movers are ascending, so an entry is found by bisection)
-__global__ void __launch_bounds__(256) k_compact_table(const Kv d, int32_t* table_out) {
+// Compaction, second launch: every table entry that names a mover names its hole
+// (the movers are ascending, so an entry is found by bisection), and the pages move
+__global__ void __launch_bounds__(256) k_compact_move(const Kv d, int32_t* table_out) {
+  second_of_two();
   const int movers = d.hdr[H_MOVES];
   const long long n = (long long)d.max_seqs * d.max_pages;
   const int first = movers ? d.list_a[0] : 0x7fffffff;
@@ -452,6 +493,7 @@ __global__ void __launch_bounds__(256) k_compact_table(const Kv d, int32_t* tabl
     }
     table_out[i] = p;
   }
+  copy_pages(d, d.list_a, d.list_b, movers);
 }
 
 size_t bitmap_bytes(const moe_kv_pages& kv) { return ((size_t)kv.max_seqs + 31) / 32 * 4; }
@@ -474,8 +516,7 @@ cudaError_t launch_kv_reserve(const moe_kv_pages& kv, const int32_t* seqs, const
   if (e != cudaSuccess) return e;
   const long long most = (long long)n * kv.layers * 2 * kv.kv_heads;
   const int grid = device_sm_count() * 8;
-  k_copy_tails<<<most < grid ? (int)most : grid, 256, 0, s>>>(d);
-  return cudaGetLastError();
+  return launch_second(k_copy_tails, most < grid ? (int)most : grid, 256, 0, s, d);
 }
 
 cudaError_t launch_kv_append(const moe_kv_pages& kv, int layer, const int32_t* seqs, const int32_t* starts, int n,
@@ -511,13 +552,12 @@ cudaError_t launch_kv_fork(const moe_kv_pages& kv, const int32_t* src, const int
   k_fork_read<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(d, src, dst, n);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_fork_write<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(d, src, dst, n);
-  return cudaGetLastError();
+  return launch_second(k_fork_write, rows_grid(n), 256, bitmap_bytes(kv), s, d, src, dst, n);
 }
 
 cudaError_t launch_kv_copy(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
   if (n <= 0) return cudaSuccess;
-  k_copy_pages<<<device_sm_count() * 8, 256, 0, s>>>(make(kv), src, dst, n, nullptr);
+  k_copy_pages<<<device_sm_count() * 8, 256, 0, s>>>(make(kv), src, dst, n);
   return cudaGetLastError();
 }
 
@@ -525,16 +565,9 @@ cudaError_t launch_kv_compact(const moe_kv_pages& kv, int32_t* table_out, int32_
                               cudaStream_t s) {
   const Kv d = make(kv);
   k_compact_plan<<<1, kBookThreads, 0, s>>>(d, refs_out, used);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_copy_pages<<<device_sm_count() * 8, 256, 0, s>>>(d, d.list_a, d.list_b, 0, d.hdr + H_MOVES);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const long long n = (long long)kv.max_seqs * kv.max_pages;
-  const long long want = (n + 255) / 256;
-  const int most = device_sm_count() * 8;
-  k_compact_table<<<(int)(want < most ? want : most), 256, 0, s>>>(d, table_out);
-  return cudaGetLastError();
+  return launch_second(k_compact_move, device_sm_count() * 8, 256, 0, s, d, table_out);
 }
 
 }  // namespace moe
