@@ -620,11 +620,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int x = 0; x < DP / 16; ++x) {
               const uint32_t o = ((x / 4) * S::kBox + (x % 4) * 32) >> 4;
+              // half way: the other thread wakes up while the rest is issued
+              if (x == DP / 32 && j >= begin) arrive(tc::smem_u32(&c.turn[i ^ 1]));
               tc::mma_bf16(ts, dq + o, kk + o, id_s, x > 0);
             }
             tc::mma_commit(tc::smem_u32(&c.sfull[i]));
+          } else if (j >= begin) {
+            arrive(tc::smem_u32(&c.turn[i ^ 1]));
           }
-          if (j >= begin) arrive(tc::smem_u32(&c.turn[i ^ 1]));
           if (j + 2 == last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
           if (j + 1 == last && last > 0) tc::mma_commit(tc::smem_u32(&c.ofull[i]));
           if (j + 1 < end) {
