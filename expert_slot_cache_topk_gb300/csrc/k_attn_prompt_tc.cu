@@ -19,7 +19,7 @@
 //                    One thread each, so one tile's waits and bookkeeping run
 //                    under the other's products;
 //   warp 9           finds the items and loads Q, K and V by TMA (128-byte swizzle);
-//   warp 11          passes the values on, cleaned in steps that a mask crosses (below);
+//   warp 11          passes the values on, cleaned where that is asked for (below);
 //   warps 12-15      scale both tiles' O by 1 / l and store them, while the softmax
 //                    warps are at the next item.
 // Tensor memory, 512 columns: S0 S1 (128 each, P over the first half of each)
@@ -31,12 +31,16 @@
 // precision), so O is rescaled a few times per row at most; that happens in
 // tensor memory between S(j) and PV(j), when no MMA touches O.
 //
-// Masks: only tiles that the causal diagonal, the window or the sequence's end
-// crosses are masked (scores become -inf).  A weight of 0 times a value that is
-// not finite would still give NaN, so in those steps a warp zeroes, in shared
-// memory, the values past the sequence's end and every value that is not finite;
-// the rows that do see such a value are computed again with plain arithmetic
-// that never touches hidden keys (redo_row).  Other rows keep their bits.
+// Masks: only steps that the causal diagonal, the window or the sequence's end
+// crosses are masked (scores become -inf).  A weight of 0 times a value that is not
+// finite would still give NaN.  So a result that is not finite is not taken at once:
+// its item is put aside and done again, carefully, when the others are through (and
+// items found from then on are done carefully at once).  Carefully means that in
+// crossed steps a warp zeroes, in shared memory, the values past the sequence's end
+// and every value that is not finite; the rows that do see such a value are computed
+// with plain arithmetic that never touches hidden keys (redo_row).  Other rows get
+// the bits that they would have without it.  (Cleaning every crossed step at once
+// cost 24 packed prompts of up to 1500 tokens 149 us instead of 129.)
 #include <cuda.h>
 #include <cmath>
 
@@ -94,6 +98,7 @@ struct Item {
   Tile t[2];
   int off, first, last;          // last key of query r: r + off; steps of the item
   int clean_from, clean_to;      // steps in [clean_from, clean_to) are crossed by no mask
+  int unit, careful, again;      // of the grid; clean the values; a result was not finite
   int bad_lo, bad_hi;            // keys (of the sequence) with a value that was zeroed: first, last
 };
 
@@ -107,6 +112,7 @@ struct Ctl {
   float2 sums[2][128];           // [tile][row]: m and l of finished rows
   uint32_t tmem;
   int stop;
+  int careful, put_aside, aside[2];   // an item was put aside; how many (this one and the one under way, at most)
 };
 constexpr int kItemReaders = 15;                   // two MMA threads, the cleaning warp, eight softmax and four storing warps
 
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::mbar_init(tc::smem_u32(&c.vempty[i]), 2);
     }
     tc::mbar_init(tc::smem_u32(&c.next), 1);
-    c.stop = 0;
+    c.stop = 0, c.careful = 0, c.put_aside = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&c.tmem), 512);
@@ -415,9 +421,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       Ring<S::kKeyRing> rk;                            // the next K and V loads
       Ring<S::kValRing> rv;
       bool ok = true;
+      bool drawing = true;                             // units come from the grid; then those put aside
+      int redone = 0;
       while (ok) {
         Item it;
         it.live = 1, it.bad_lo = 0x7fffffff, it.bad_hi = -1;
+        it.unit = unit, it.again = 0;
         it.head = unit % per_slot * a.pack;
         const int slot = a.slots - 1 - unit / per_slot;
         int lo = 0, hi = a.n;                          // the last sequence whose tiles start at or before the slot
@@ -438,6 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int z = published & 1;
           if (published >= 2) ok = warp_wait(c, c.iempty[z], (published / 2 - 1) & 1);
           if (!ok) break;
+          it.careful = *reinterpret_cast<volatile int*>(&c.careful);
           if (lane == 0) {
             c.item[z] = it;
             arrive(tc::smem_u32(&c.ifull[z]));
@@ -477,6 +487,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ok = __shfl_sync(kAll, ok, 0);
         }
         if (!ok) break;
+        if (!drawing) {
+          if (redone == *reinterpret_cast<volatile int*>(&c.put_aside)) break;
+          unit = c.aside[redone++];
+          continue;
+        }
         // ask for the next unit once this one's loads are out (earlier, and a block would
         // hold long units that an idle one could take)
         if (lane == 0) {
@@ -502,9 +517,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             : "=r"(took), "=r"(bx)
             : "r"(tc::smem_u32(c.cancel))
             : "memory");
-        if (!took) break;
         unit = (int)bx;
         __syncwarp();
+        if (!took) {                                   // no more: wait for the items under way, then those put aside
+          for (unsigned x = published > 2 ? published - 2 : 0; x < published && ok; ++x)
+            ok = warp_wait(c, c.iempty[x & 1], (x / 2) & 1);
+          drawing = false;
+          if (!ok || *reinterpret_cast<volatile int*>(&c.put_aside) == 0) break;
+          unit = c.aside[redone++];
+        }
       }
       if (ok) {                                        // tell the others that there is no more
         const int z = published & 1;
@@ -532,11 +553,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         Item& it = c.item[n & 1];
         if (!it.live) break;
         const int first = it.first, last = it.last, clean_from = it.clean_from, clean_to = it.clean_to;
-        const int lk = it.lk;
+        const int lk = it.lk, careful = it.careful;
         for (int j = first; j < last; ++j) {
           ok = warp_wait(c, c.vfull[rv.slot], rv.turn);
           if (!ok) break;
-          if (j < clean_from || j >= clean_to) clean<DP>(vring + rv.slot * S::kTile, lane, j * kKeys, lk, it);
+          if (careful && (j < clean_from || j >= clean_to)) clean<DP>(vring + rv.slot * S::kTile, lane, j * kKeys, lk, it);
           if (lane == 0) arrive(tc::smem_u32(&c.vready[rv.slot]));
           rv.next();
         }
@@ -781,6 +802,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::fence_after_sync();
         const bool mine = row < it.lq && row_token < tt && !sees_zeroed(it, at, window);   // (those: redo_row)
         const bool some = w.last > 0 && !(l == 0.f);
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+        __nv_bfloat162 look = zero;
         const float f = !ok ? NAN : some ? 1.f / l : 0.f;
         // the rows of the quad: row quarter ^ y of it, null where there is none
         __nv_bfloat16* to[4];
@@ -802,7 +825,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int y = 0; y < 32; ++y) o[y] = 0u;
           }
 #pragma unroll
-          for (int y = 0; y < 16; ++y) o[y] = pack_bf16(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+          for (int y = 0; y < 16; ++y) {
+            o[y] = pack_bf16(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+            look = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&o[y]), zero, look);     // 0, or NaN once a value is not finite
+          }
           // The four lanes of a quad exchange 16-byte pieces, so that each store writes 64
           // bytes of eight rows instead of 16 bytes of 32: lane q of the quad gets piece q
           // of every row of the quad, row q ^ y in piece y.
@@ -827,6 +853,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (w.last > 0 && lane == 0) arrive(tc::smem_u32(&c.oempty[i]));
+        const float odd = __low2float(look) + __high2float(look);
+        if (!it.careful && __any_sync(kAll, mine && odd != 0.f) && lane == 0 && atomicExch(&c.item[n & 1].again, 1) == 0) {
+          c.aside[atomicAdd(&c.put_aside, 1)] = it.unit;
+          c.careful = 1;                                  // seen by whoever waits for this item's release
+        }
         if (mine && a.lse)
           a.lse[(long long)(it.q0 + row) * a.heads + head] = !ok ? NAN : some ? (m == -INFINITY ? 0.f : m) * kLn2 + logf(l) : -INFINITY;
       }

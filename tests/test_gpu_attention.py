@@ -591,6 +591,27 @@ def test_prompt_values_behind_the_mask_do_not_matter(A, dtype, bad, dim):
     assert not torch.isfinite(out[hit]).any()
 
 
+@pytest.mark.parametrize("every", [1, 3])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_values_behind_the_mask_in_many_tiles(A, dim, every):
+    """The same where every block has several tiles to do, and all of them or every third sequence hold such values:
+    at a sequence's end (its last query alone sees it) and in its middle."""
+    g = gen(2)
+    lens = [(700, 700)] * 40
+    q, k, v, sq, sk = prompt_inputs(g, lens, 8, 4, dim, torch.bfloat16)
+    clean = torch.empty_like(q)
+    A.attn_prompt(q, k, v, sq, sk, clean)
+    hit = torch.zeros(q.shape[0], dtype=torch.bool)
+    for i in range(0, len(lens), every):
+        at = 700 * i + (699 if i % 2 else 333)
+        v[at] = math.inf if i % 4 < 2 else math.nan
+        hit[at:700 * (i + 1)] = True
+    out = torch.empty_like(q)
+    A.attn_prompt(q, k, v, sq, sk, out)
+    assert torch.equal(bits(out[~hit]), bits(clean[~hit]))
+    assert not torch.isfinite(out[hit]).any()
+
+
 def test_prompt_refusals(A):
     from expert_slot_cache_topk_gb300._abi import MoeError
     q = torch.zeros(4, 4, 64, dtype=BF, device="cuda")
