@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         const Item& it = c.item[n & 1];
         const int live = it.live, first = it.t[i].first, last = it.t[i].last, begin = it.first, end = it.last;
+        const int first2 = it.t[i ^ 1].first, last2 = it.t[i ^ 1].last;
         arrive(tc::smem_u32(&c.iempty[n & 1]));
         if (!live) break;
         if (last > 0) {
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // S(first .. last - 1) and PV in turn; the other steps' tiles are only passed on
         for (int j = begin - 1; j < end && ok; ++j) {
-          const bool pv = j >= first && j < last, sc = j + 1 >= first && j + 1 < last;
+          const bool pv = j >= first && j < last, both = pv && j >= first2 && j < last2, sc = j + 1 >= first && j + 1 < last;
           if (j >= begin) ok = wait(c.vready[rv.slot], rv.turn) && wait(c.vfull[rv.slot], rv.turn);
           if (j + 1 < end && ok) ok = wait(c.kfull[rk.slot], rk.turn);
           // the weights come in two halves: the first 64 keys' product runs while
@@ -615,9 +616,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               no ^= 1;
             }
             tc::fence_after_sync();
-            // the tiles take turns from here to the scores, so that one's products
-            // run under the other's softmax
-            if (ok) ok = wait(c.turn[i], my);
+            // where both are at work, the tiles take turns from here to the scores, so
+            // that one's products run under the other's softmax
+            if (ok && both) {
+              ok = wait(c.turn[i], my);
+              my ^= 1;
+            }
             if (ok) {
 #pragma unroll
               for (int x = 0; x < 4; ++x)
@@ -626,10 +630,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               np ^= 1;
               tc::fence_after_sync();
             }
-          }
-          if (j >= begin) {
-            if (ok && !pv) ok = wait(c.turn[i], my);
-            my ^= 1;
           }
           if (!ok) break;
           if (pv) {
@@ -642,11 +642,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int x = 0; x < DP / 16; ++x) {
               const uint32_t o = ((x / 4) * S::kBox + (x % 4) * 32) >> 4;
               // half way: the other thread wakes up while the rest is issued
-              if (x == DP / 32 && j >= begin) arrive(tc::smem_u32(&c.turn[i ^ 1]));
+              if (x == DP / 32 && both) arrive(tc::smem_u32(&c.turn[i ^ 1]));
               tc::mma_bf16(ts, dq + o, kk + o, id_s, x > 0);
             }
             tc::mma_commit(tc::smem_u32(&c.sfull[i]));
-          } else if (j >= begin) {
+          } else if (both) {
             arrive(tc::smem_u32(&c.turn[i ^ 1]));
           }
           if (j + 2 == last) tc::mma_commit(tc::smem_u32(&c.qempty[i]));
