@@ -612,6 +612,26 @@ def test_prompt_values_behind_the_mask_in_many_tiles(A, dim, every):
     assert not torch.isfinite(out[hit]).any()
 
 
+@pytest.mark.parametrize("dim", [40, 64, 128, 256])
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("bad", [0.0, math.inf])
+def test_prompt_f32_with_many_heads(A, dim, window, bad):
+    """Enough work for the larger tiles of every head size; `bad` is a value behind the mask of most queries."""
+    g = gen(3)
+    lens = [(500, 700), (33, 20), (0, 5), (1, 300)]
+    q, k, v, sq, sk = prompt_inputs(g, lens, 32, 8, dim, F32)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    A.attn_prompt(q, k, v, sq, sk, out, window=window, lse=lse)
+    check_prompt(q, k, v, lens, out, lse, dim ** -0.5, window)
+    v[200 + 450, 3] = bad                                          # seen by the queries from 450 on, heads 12 to 15
+    again = torch.empty_like(q)
+    A.attn_prompt(q, k, v, sq, sk, again, window=window)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool)
+    hit[450:min(500, 450 + (window or 500)), 12:16] = True
+    assert torch.equal(bits(again[~hit]), bits(out[~hit]))
+    assert bool(torch.isfinite(again[hit]).any()) == (bad == 0.0)
+
+
 def test_prompt_refusals(A):
     from expert_slot_cache_topk_gb300._abi import MoeError
     q = torch.zeros(4, 4, 64, dtype=BF, device="cuda")
