@@ -101,6 +101,8 @@ def norm_residual(x, block=None, pre_weight=None, x_out=None, y=None, post_weigh
     """
     code = _hidden_type(x)
     dtype, device, shape = x.dtype, x.get_device(), x.shape
+    if device < 0:
+        raise TypeError("x must be a CUDA tensor")
     if len(shape) != 2:
         raise ValueError("x must have shape [tokens, hidden]")
     T, H = shape
@@ -151,6 +153,8 @@ def attn_prompt(q, k, v, starts_q, starts_k, out, scale=None, window=0, lse=None
     """
     code = _hidden_type(q)
     dtype, device, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
+    if device < 0:
+        raise TypeError("q must be a CUDA tensor")
     if len(qs) != 3 or len(ks) != 3:
         raise ValueError("q, k and v must have shape [tokens, heads, head_dim]")
     Tq, Hq, D = qs

@@ -104,3 +104,17 @@ def test_bad_prompts_and_norms_are_refused(abi):
                dict(x_d=None), dict(pre_w_d=None), dict(x_out_d=None, y_d=None), dict(y_d=4096), dict(gate_col=2),
                dict(block_d=None, post_w_d=4096), dict(y_row=63), dict(x_row=128), dict(x_d=4098), dict(x_row=-1)):
         refused(abi, L.moe_norm_residual(abi.moe_norm_args(**{**norm, **kw}), None))
+
+
+def test_tensors_in_host_memory_are_refused():
+    import torch
+    from expert_slot_cache_topk_gb300 import attention as A
+    x, w = torch.zeros(2, 64), torch.zeros(64)
+    with pytest.raises(TypeError, match="CUDA"):
+        A.norm_residual(x, x, w, x, torch.zeros(2, 64))
+    q, starts = torch.zeros(3, 2, 64), torch.tensor([0, 3], dtype=torch.int32)
+    with pytest.raises(TypeError, match="CUDA"):
+        A.attn_prompt(q, q, q, starts, starts, torch.zeros_like(q))
+    pool, ints = torch.zeros(1, 4, 2, 16, 64), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(TypeError, match="CUDA"):
+        A.KVPages(pool, pool.clone(), ints.view(2, 2), ints[:2], ints)
