@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(128, DP == 64 ? 2 : 1) k_prompt_keys(const moe
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = lane >> 3, kg = lane & 7;
   float* K = sm + BM * PIT + warp * kWarp;                   // [BK][PIT]; the warp's output in the end
   float* V = K + BK * PIT;                                   // [BK][PIT]
-  float* P = V + BK * PIT;                                   // [BM][PP], each weight twice; the warp's maxima and sums in the end
+  float* P = V + BK * PIT;                                   // [BM][PP], each weight twice; maxima and sums in the end
   const int h = blockIdx.x % a.heads, kh = h / (a.heads / a.kv_heads), D = a.head_dim;
   int r0;                                      // late tiles, the long ones, first
   const int seq = tile_sequence(a.starts_q_d, a.n, a.q_tokens / BM + a.n - 1 - (int)(blockIdx.x / a.heads), BM, &r0);

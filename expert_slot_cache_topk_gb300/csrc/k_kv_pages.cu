@@ -4,8 +4,12 @@
 // whose lists are wrong sets the status word and changes nothing.
 //
 // What bounds these calls: the bookkeeping is a few kilobytes and costs
-// launches and dependent loads; append, the private copies of shared pages and
-// compaction move K and V bytes once (read + write).
+// launches and dependent loads (64 sequences truncated, given room for 3 tokens and
+// appended to: 19 us for the three calls).  Append, the private copies of shared pages
+// and compaction move K and V bytes once (read + write): 56 copied pages of 16 layers
+// 102 us with the calls around them (585 MB), 4099 pages compacted 337 us (2.1 GB, 6.3
+// TB/s).  A second kernel is launched while the first runs (programmatic dependent
+// launch) and waits for it before it reads what the first writes.
 #include "attn_common.cuh"
 
 namespace moe {
