@@ -11,8 +11,6 @@ nothing is allocated in a call except where its docstring says so.
 from __future__ import annotations
 
 import ctypes as C
-import struct
-from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -25,25 +23,6 @@ _byref = C.byref
 
 # The checks run at every call, next to kernels of a few microseconds: they read
 # each attribute once and build their messages only when they refuse.
-
-_CODES = {C.c_int: "i", C.c_longlong: "q", C.c_void_p: "P", C.c_float: "f"}
-
-
-def _packer(args):
-    """Packs a struct's fields into bytes (null pointers as 0): a fifth of the time that filling the ctypes
-    struct takes."""
-    f = struct.Struct("@" + "".join(_CODES[kind] for _, kind in args._fields_))
-    return struct.Struct(f.format + "x" * (C.sizeof(args) - f.size)).pack
-
-
-_norm_args, _prompt_args = _packer(_abi.moe_norm_args), _packer(_abi.moe_prompt_args)
-
-
-@lru_cache(maxsize=None)
-def _entry(name):
-    """The entry point (arguments' bytes, stream) -> status."""
-    return C.CFUNCTYPE(C.c_int, C.c_char_p, C.c_void_p)((name, _abi.lib()))
-
 
 def _hidden_type(t: torch.Tensor) -> int:
     code = _DTYPE.get(t.dtype)
@@ -127,10 +106,8 @@ def norm_residual(x, block=None, pre_weight=None, x_out=None, y=None, post_weigh
     if len(shape) != 2:
         raise ValueError("x must have shape [tokens, hidden]")
     T, H = shape
-    x_row, col = x.stride()
-    if col != 1 and H > 1:
-        raise ValueError("x: rows must be contiguous")
-    b = xo = yo = pw = w = g = 0
+    xp, x_row = _rows(x, x, dtype, device, shape, "x")
+    b = xo = yo = pw = w = g = None
     b_row = xo_row = yo_row = g_row = g_col = 0
     if block is not None:
         b, b_row = _rows(block, x, dtype, device, shape, "block")
@@ -158,8 +135,8 @@ def norm_residual(x, block=None, pre_weight=None, x_out=None, y=None, post_weigh
             if col != 1:
                 raise ValueError("gate rows must be contiguous")
         g = gate.data_ptr()
-    a = _norm_args(code, H, T, x.data_ptr(), b, pw, g, w, xo, yo, x_row, b_row, g_row, xo_row, yo_row, g_col, res_scale, eps)
-    _abi._check(_entry("moe_norm_residual")(a, _abi._stream(stream)))
+    a = _abi.moe_norm_args(code, H, T, xp, b, pw, g, w, xo, yo, x_row, b_row, g_row, xo_row, yo_row, g_col, res_scale, eps)
+    _abi._check(_abi.lib().moe_norm_residual(_byref(a), _abi._stream(stream)))
 
 
 def attn_prompt(q, k, v, starts_q, starts_k, out, scale=None, window=0, lse=None, stream=None):
@@ -182,20 +159,18 @@ def attn_prompt(q, k, v, starts_q, starts_k, out, scale=None, window=0, lse=None
         raise ValueError("q, k and v must have shape [tokens, heads, head_dim]")
     Tq, Hq, D = qs
     Tk, Hkv, _ = ks
-    q_token, q_head, dim = q.stride()
-    if dim != 1 and D != 1:
-        raise ValueError("q: the head dimension must be contiguous")
+    qp, q_token, q_head = _heads(q, q, dtype, device, qs, "q")
     kp, k_token, k_head = _heads(k, q, dtype, device, (Tk, Hkv, D), "k")
     vp, v_token, v_head = _heads(v, q, dtype, device, ks, "v")
     op, o_token, o_head = _heads(out, q, dtype, device, qs, "out")
     n = starts_q.shape[0] - 1 if starts_q.dim() else -1
     if n < 0:
         raise ValueError("starts_q and starts_k need at least one entry")
-    a = _prompt_args(code, Hq, Hkv, D, n, Tq, Tk, _ints(starts_q, n + 1, device, "starts_q"),
-                     _ints(starts_k, n + 1, device, "starts_k"), q.data_ptr(), kp, vp, op,
-                     _lse(lse, Tq, Hq, device) or 0, q_token, q_head, k_token, k_head, v_token, v_head,
-                     o_token, o_head, D ** -0.5 if scale is None else scale, window)
-    _abi._check(_entry("moe_attn_prompt")(a, _abi._stream(stream)))
+    a = _abi.moe_prompt_args(code, Hq, Hkv, D, n, Tq, Tk, _ints(starts_q, n + 1, device, "starts_q"),
+                             _ints(starts_k, n + 1, device, "starts_k"), qp, kp, vp, op,
+                             _lse(lse, Tq, Hq, device), q_token, q_head, k_token, k_head, v_token, v_head,
+                             o_token, o_head, D ** -0.5 if scale is None else scale, window)
+    _abi._check(_abi.lib().moe_attn_prompt(_byref(a), _abi._stream(stream)))
 
 
 class KVPages:

@@ -106,14 +106,6 @@ def test_bad_prompts_and_norms_are_refused(abi):
         refused(abi, L.moe_norm_residual(abi.moe_norm_args(**{**norm, **kw}), None))
 
 
-def test_packed_arguments_have_the_structs_bytes(abi):
-    from expert_slot_cache_topk_gb300 import attention as A
-    for name, pack in (("moe_norm_args", A._norm_args), ("moe_prompt_args", A._prompt_args)):
-        cls = getattr(abi, name)
-        values = [0.5 + i if kind is ctypes.c_float else 3 * i + 1 for i, (_, kind) in enumerate(cls._fields_)]
-        assert pack(*values) == bytes(cls(*values))
-
-
 def test_tensors_in_host_memory_are_refused():
     import torch
     from expert_slot_cache_topk_gb300 import attention as A
