@@ -3,7 +3,9 @@
 Each .cu translation unit is compiled in parallel to an object under
 ``_build/`` and the objects are linked into
 ``expert_slot_cache_topk_gb300/libmoecache.so`` (CUDA runtime linked
-statically, so the library needs only the driver at run time).
+statically, so the library needs only the driver at run time).  Where torch is
+installed, csrc/torch_calls.cpp becomes the extension module ``_torch_calls``
+(the argument checks of attention.py) next to it.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoecache.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS = os.path.join(PKG, "_torch_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -41,16 +46,42 @@ def _deps() -> list:
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(path, deps) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _build_calls(force: bool) -> None:
+    headers = glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and _newer(CALLS, [CALLS_SRC, *headers]):
+        return
+    try:
+        import torch
+    except ImportError:
+        return
+    base = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), CALLS_SRC, "-o", tmp,
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = 0) -> str:
     """Compile and link; returns the library path.  Raises on any nvcc error."""
     if not force and up_to_date():
+        _build_calls(force)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -67,8 +98,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = 0) -> st
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(jobs or len(srcs)) as ex:
+    with ThreadPoolExecutor(jobs or len(srcs) + 1) as ex:
+        calls = ex.submit(_build_calls, force)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -2,9 +2,10 @@
 key-value cache, attention of one new token over it, and attention over packed
 prompts (include/moe_attn.h).
 
-Argument checks and marshalling; the work runs in the library's CUDA kernels on
-the caller's stream (``stream=None`` is the legacy default stream, as elsewhere
-in this package).  Tensors are torch tensors on one CUDA device, bf16 or f32;
+Argument checks and marshalling (in csrc/torch_calls.cpp: calls of few tokens are
+bound by them); the work runs in the library's CUDA kernels on the caller's
+stream (``stream=None`` is the legacy default stream, as elsewhere in this
+package).  Tensors are torch tensors on one CUDA device, bf16 or f32;
 nothing is allocated in a call except where its docstring says so.
 """
 
@@ -19,72 +20,35 @@ from . import _abi
 
 _DTYPE = {torch.bfloat16: _abi.MOE_BF16, torch.float32: _abi.MOE_F32}
 _byref = C.byref
+_calls = None
 
 
-# The checks run at every call, next to kernels of a few microseconds: they read
-# each attribute once and build their messages only when they refuse.
-
-def _hidden_type(t: torch.Tensor) -> int:
-    code = _DTYPE.get(t.dtype)
-    if code is None:
-        raise TypeError(f"expected a bfloat16 or float32 tensor, got {t.dtype}")
-    return code
-
-
-def _wrong_kind(t, ref, what):
-    raise TypeError(f"{what} must be a {ref.dtype} tensor on {ref.device}, got {t.dtype} on {t.device}")
-
-
-def _rows(t, x, dtype, device, shape, what):
-    """(address, row distance) of a tensor with x's type, place and shape and contiguous rows."""
-    if t.dtype is not dtype or t.get_device() != device:
-        _wrong_kind(t, x, what)
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
-    row, col = t.stride()
-    if col != 1 and shape[1] > 1:
-        raise ValueError(f"{what}: rows must be contiguous")
-    return t.data_ptr(), row
+def _load():
+    """The extension module of the calls, bound to the library's entry points; raises if it is missing."""
+    global _calls
+    L = _abi.lib()
+    try:
+        from . import _torch_calls
+    except ImportError as e:
+        raise RuntimeError("the _torch_calls extension is not built for this Python and torch; run "
+                           "`python -c \"import __graft_entry__ as g; g.build()\"`") from e
+    _torch_calls.bind(*(_entry(L, name) for name in ("moe_norm_residual", "moe_attn_prompt", "moe_attn_decode",
+                                                     "moe_kv_append")))
+    _calls = _torch_calls
+    return _calls
 
 
-def _vector(t, x, dtype, device, n, what):
-    """Address of a contiguous vector of n entries with x's type and place."""
-    if t.dtype is not dtype or t.get_device() != device:
-        _wrong_kind(t, x, what)
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride()[0] != 1):
-        raise ValueError(f"{what} must be a contiguous vector of {n} entries")
-    return t.data_ptr()
+def _entry(L, name) -> int:
+    return C.cast(getattr(L, name), C.c_void_p).value
 
 
-def _ints(t: torch.Tensor, n: Optional[int], device: int, what: str) -> int:
+def _ints(t: torch.Tensor, n: int, device: int, what: str) -> int:
     """Address of a contiguous int32 vector of n entries."""
-    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise TypeError(f"{what} must be an int32 vector" + ("" if n is None else f" of {n} entries")
-                        + f" on device {device}")
-    if t.stride()[0] != 1 and t.shape[0] > 1:
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or t.shape[0] != n:
+        raise TypeError(f"{what} must be an int32 vector of {n} entries on device {device}")
+    if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
-
-
-def _heads(t, ref, dtype, device, shape, what: str):
-    """(address, token distance, head distance) of a [tokens, heads, head_dim] tensor of ref's type and place."""
-    if t.dtype is not dtype or t.get_device() != device:
-        _wrong_kind(t, ref, what)
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
-    token, head, dim = t.stride()
-    if dim != 1 and shape[2] != 1:
-        raise ValueError(f"{what}: the head dimension must be contiguous")
-    return t.data_ptr(), token, head
-
-
-def _lse(lse: Optional[torch.Tensor], n: int, heads: int, device: int) -> Optional[int]:
-    if lse is None:
-        return None
-    if lse.dtype is not torch.float32 or lse.get_device() != device or lse.shape != (n, heads) or \
-            not lse.is_contiguous():
-        raise TypeError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on device {device}")
-    return lse.data_ptr()
 
 
 def norm_residual(x, block=None, pre_weight=None, x_out=None, y=None, post_weight=None, gate=None, res_scale=1.0,
@@ -99,44 +63,9 @@ def norm_residual(x, block=None, pre_weight=None, x_out=None, y=None, post_weigh
     None, and may be x or block themselves.  gate: None, [tokens, 1] (one per
     token), [1, hidden] or [hidden] (one per channel), or [tokens, hidden].
     """
-    code = _hidden_type(x)
-    dtype, device, shape = x.dtype, x.get_device(), x.shape
-    if device < 0:
-        raise TypeError("x must be a CUDA tensor")
-    if len(shape) != 2:
-        raise ValueError("x must have shape [tokens, hidden]")
-    T, H = shape
-    xp, x_row = _rows(x, x, dtype, device, shape, "x")
-    b = xo = yo = pw = w = g = None
-    b_row = xo_row = yo_row = g_row = g_col = 0
-    if block is not None:
-        b, b_row = _rows(block, x, dtype, device, shape, "block")
-    if x_out is not None:
-        xo, xo_row = _rows(x_out, x, dtype, device, shape, "x_out")
-    if y is not None:
-        yo, yo_row = _rows(y, x, dtype, device, shape, "y")
-    if post_weight is not None:
-        pw = _vector(post_weight, x, dtype, device, H, "post_weight")
-    if pre_weight is not None:
-        w = _vector(pre_weight, x, dtype, device, H, "pre_weight")
-    if gate is not None:
-        if gate.dtype is not dtype or gate.get_device() != device:
-            _wrong_kind(gate, x, "gate")
-        gs = gate.shape
-        if len(gs) == 1:
-            gate, gs = gate[None], (1, gs[0])
-        if len(gs) != 2 or gs[0] not in (1, T) or gs[1] not in (1, H):
-            raise ValueError(f"gate must broadcast to {[T, H]}")
-        g_row, col = gate.stride()
-        if gs[0] == 1:
-            g_row = 0
-        if gs[1] > 1:
-            g_col = 1
-            if col != 1:
-                raise ValueError("gate rows must be contiguous")
-        g = gate.data_ptr()
-    a = _abi.moe_norm_args(code, H, T, xp, b, pw, g, w, xo, yo, x_row, b_row, g_row, xo_row, yo_row, g_col, res_scale, eps)
-    _abi._check(_abi.lib().moe_norm_residual(_byref(a), _abi._stream(stream)))
+    st = (_calls or _load()).norm(x, block, pre_weight, x_out, y, post_weight, gate, res_scale, eps, stream)
+    if st:
+        _abi._check(st)
 
 
 def attn_prompt(q, k, v, starts_q, starts_k, out, scale=None, window=0, lse=None, stream=None):
@@ -151,26 +80,9 @@ def attn_prompt(q, k, v, starts_q, starts_k, out, scale=None, window=0, lse=None
     head_dim ** -0.5.  lse: float32 [q_tokens, heads] or None.  A query that sees
     nothing gives zeros and lse = -inf.
     """
-    code = _hidden_type(q)
-    dtype, device, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
-    if device < 0:
-        raise TypeError("q must be a CUDA tensor")
-    if len(qs) != 3 or len(ks) != 3:
-        raise ValueError("q, k and v must have shape [tokens, heads, head_dim]")
-    Tq, Hq, D = qs
-    Tk, Hkv, _ = ks
-    qp, q_token, q_head = _heads(q, q, dtype, device, qs, "q")
-    kp, k_token, k_head = _heads(k, q, dtype, device, (Tk, Hkv, D), "k")
-    vp, v_token, v_head = _heads(v, q, dtype, device, ks, "v")
-    op, o_token, o_head = _heads(out, q, dtype, device, qs, "out")
-    n = starts_q.shape[0] - 1 if starts_q.dim() else -1
-    if n < 0:
-        raise ValueError("starts_q and starts_k need at least one entry")
-    a = _abi.moe_prompt_args(code, Hq, Hkv, D, n, Tq, Tk, _ints(starts_q, n + 1, device, "starts_q"),
-                             _ints(starts_k, n + 1, device, "starts_k"), qp, kp, vp, op,
-                             _lse(lse, Tq, Hq, device), q_token, q_head, k_token, k_head, v_token, v_head,
-                             o_token, o_head, D ** -0.5 if scale is None else scale, window)
-    _abi._check(_abi.lib().moe_attn_prompt(_byref(a), _abi._stream(stream)))
+    st = (_calls or _load()).prompt(q, k, v, starts_q, starts_k, out, scale, window, lse, stream)
+    if st:
+        _abi._check(st)
 
 
 class KVPages:
@@ -188,9 +100,11 @@ class KVPages:
     """
 
     def __init__(self, k, v, table, lens, refs, max_heads: Optional[int] = None):
-        code = _hidden_type(k)
+        code = _DTYPE.get(k.dtype)
+        if code is None:
+            raise TypeError(f"expected a bfloat16 or float32 tensor, got {k.dtype}")
         if v.dtype is not k.dtype or v.device != k.device:
-            _wrong_kind(v, k, "v")
+            raise TypeError(f"v must be a {k.dtype} tensor on {k.device}, got {v.dtype} on {v.device}")
         if k.dim() != 5 or v.shape != k.shape or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("k and v must be contiguous [layers, num_pages, kv_heads, page_tokens, head_dim]")
         if not k.is_cuda:
@@ -201,7 +115,7 @@ class KVPages:
         seqs, columns = table.shape
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
         self.device = k.device
-        self._dev, self._dtype = k.get_device(), k.dtype
+        self._dev = k.get_device()
         self.kv_heads, self.head_dim, self.max_seqs, self.num_pages = kv_heads, dim, seqs, pages
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._kv = _abi.moe_kv_pages(code, layers, kv_heads, dim, page, pages, seqs, columns, k.data_ptr(), v.data_ptr(),
@@ -213,7 +127,10 @@ class KVPages:
         self._work = torch.zeros(need.value, dtype=torch.uint8, device=k.device)
         self._kv.work_d, self._kv.work_bytes = self._work.data_ptr(), need.value
         torch.cuda.current_stream(k.device).synchronize()     # the zeros are there for any stream
-        self._ref = _byref(self._kv)
+        self._ref, self._at = _byref(self._kv), C.addressof(self._kv)
+        L = _abi.lib()
+        self._reserve, self._truncate, self._fork, self._copy = (
+            _entry(L, name) for name in ("moe_kv_reserve", "moe_kv_truncate", "moe_kv_fork", "moe_kv_copy"))
 
     @classmethod
     def empty(cls, layers, kv_heads, head_dim, page_tokens, num_pages, max_seqs, max_pages, dtype=torch.bfloat16,
@@ -225,50 +142,39 @@ class KVPages:
                    torch.full((max_seqs, max_pages), -1, **ints), torch.zeros(max_seqs, **ints),
                    torch.zeros(num_pages, **ints), max_heads)
 
-    def _list(self, t, what, n=None) -> int:
-        return _ints(t, n, self._dev, what)
+    def _lists(self, entry, a, b, a_name, b_name, stream):
+        st = (_calls or _load()).lists(self._at, self.k, entry, a, b, a_name, b_name, stream)
+        if st:
+            _abi._check(st)
 
     def reserve(self, seqs, counts, stream=None):
         """Room for counts[i] more tokens in sequence seqs[i] (distinct rows).  New pages are the lowest free
         ones, in list order; a shared, partly filled last page becomes a private copy first."""
-        n = seqs.shape[0]
-        _abi._check(_abi.lib().moe_kv_reserve(self._ref, self._list(seqs, "seqs"), self._list(counts, "counts", n), n,
-                                              _abi._stream(stream)))
+        self._lists(self._reserve, seqs, counts, "seqs", "counts", stream)
 
     def append(self, layer, seqs, starts, k, v, stream=None):
         """Write one layer's keys and values of the newest tokens: rows starts[i] : starts[i + 1] of k and v
         [tokens, kv_heads, head_dim] are the last tokens of sequence seqs[i] (room was reserved for them)."""
-        n, T = seqs.shape[0], k.shape[0]
-        shape = (T, self.kv_heads, self.head_dim)
-        kp, kt, kh = _heads(k, self.k, self._dtype, self._dev, shape, "k")
-        vp, vt, vh = _heads(v, self.k, self._dtype, self._dev, shape, "v")
-        _abi._check(_abi.lib().moe_kv_append(self._ref, layer, self._list(seqs, "seqs"),
-                                             self._list(starts, "starts", n + 1), n, kp, kt, kh, vp, vt, vh, T,
-                                             _abi._stream(stream)))
+        st = (_calls or _load()).append(self._at, self.k, layer, seqs, starts, k, v, stream)
+        if st:
+            _abi._check(st)
 
     def truncate(self, seqs, lens, stream=None):
         """Keep the first min(held, lens[i]) tokens of sequence seqs[i]; release the pages past them."""
-        n = seqs.shape[0]
-        _abi._check(_abi.lib().moe_kv_truncate(self._ref, self._list(seqs, "seqs"), self._list(lens, "lens", n), n,
-                                               _abi._stream(stream)))
+        self._lists(self._truncate, seqs, lens, "seqs", "lens", stream)
 
     def free(self, seqs, stream=None):
         """Release everything that the listed sequences hold."""
-        _abi._check(_abi.lib().moe_kv_truncate(self._ref, self._list(seqs, "seqs"), None, seqs.shape[0],
-                                               _abi._stream(stream)))
+        self._lists(self._truncate, seqs, None, "seqs", "", stream)
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] becomes a copy of src[i] that shares its pages (dst distinct; all sources are read
         as they were before the call)."""
-        n = src.shape[0]
-        _abi._check(_abi.lib().moe_kv_fork(self._ref, self._list(src, "src"), self._list(dst, "dst", n), n,
-                                           _abi._stream(stream)))
+        self._lists(self._fork, src, dst, "src", "dst", stream)
 
     def copy(self, src_pages, dst_pages, stream=None):
         """Copy whole pages dst_pages[i] <- src_pages[i] in every layer; table and counts stay."""
-        n = src_pages.shape[0]
-        _abi._check(_abi.lib().moe_kv_copy(self._ref, self._list(src_pages, "src_pages"),
-                                           self._list(dst_pages, "dst_pages", n), n, _abi._stream(stream)))
+        self._lists(self._copy, src_pages, dst_pages, "src_pages", "dst_pages", stream)
 
     def compact(self, table_out=None, refs_out=None, used=None, stream=None):
         """Move the used pages to the front of the pool.  The table and counts that hold afterwards go to
@@ -279,23 +185,17 @@ class KVPages:
                 table_out.device != self.device or not table_out.is_contiguous():
             raise TypeError("table_out must be an int32 tensor like the cache's table")
         _abi._check(_abi.lib().moe_kv_compact(self._ref, table_out.data_ptr(),
-                                              self._list(refs_out, "refs_out", self.num_pages),
-                                              None if used is None else self._list(used, "used", 1),
+                                              _ints(refs_out, self.num_pages, self._dev, "refs_out"),
+                                              None if used is None else _ints(used, 1, self._dev, "used"),
                                               _abi._stream(stream)))
 
     def attend(self, layer, q, seqs, out, scale=None, window=0, lse=None, stream=None):
         """Attention of one new token per sequence: q, out [n, heads, head_dim]; row i reads sequence seqs[i]
         (rows may repeat), its last `window` tokens if window > 0.  scale defaults to head_dim ** -0.5.
         lse: float32 [n, heads] or None.  A sequence without tokens gives zeros and lse = -inf."""
-        if q.dim() != 3:
-            raise ValueError("q must have shape [n, heads, head_dim]")
-        n, heads, _ = q.shape
-        shape = (n, heads, self.head_dim)
-        qp, qt, qh = _heads(q, self.k, self._dtype, self._dev, shape, "q")
-        op, ot, oh = _heads(out, self.k, self._dtype, self._dev, shape, "out")
-        _abi._check(_abi.lib().moe_attn_decode(self._ref, layer, qp, qt, qh, self._list(seqs, "seqs", n), n, heads,
-                                               self.head_dim ** -0.5 if scale is None else scale, window, op, ot, oh,
-                                               _lse(lse, n, heads, self._dev), _abi._stream(stream)))
+        st = (_calls or _load()).attend(self._at, self.k, layer, q, seqs, out, scale, window, lse, stream)
+        if st:
+            _abi._check(st)
 
     def check(self, stream=None):
         """Synchronise the stream; raise MoeError (MOE_ESTATE) if a call was refused on the device since the

@@ -1,0 +1,331 @@
+// The calls of attention.py: arguments checked on torch tensors and handed to the C
+// entry points of moe_attn.h.  Written against torch's C++ tensors because a call of
+// few tokens is bound by the caller: with the same checks in Python a norm took 14.5
+// us, outputs' allocation and launch included, of which the kernel is 3.
+//
+// A function returns the entry point's status; a wrong argument raises TypeError or
+// ValueError before any of the library is called.  The entry points' addresses come
+// from the library that the ctypes binding loaded (bind).
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+#include <string>
+
+#include "moe_attn.h"
+
+namespace {
+
+struct Refused {
+  PyObject* type;
+  std::string why;
+};
+[[noreturn]] void refuse_type(const std::string& why) { throw Refused{PyExc_TypeError, why}; }
+[[noreturn]] void refuse_value(const std::string& why) { throw Refused{PyExc_ValueError, why}; }
+struct Raised {};                                   // a Python error is already set
+
+using Name = const char*;
+
+std::string attribute(const at::Tensor& t, Name name) {        // as Python prints it, for messages
+  std::string out = "?";
+  PyObject* o = THPVariable_Wrap(t);
+  PyObject* v = o ? PyObject_GetAttrString(o, name) : nullptr;
+  PyObject* s = v ? PyObject_Str(v) : nullptr;
+  if (s && PyUnicode_AsUTF8(s)) out = PyUnicode_AsUTF8(s);
+  Py_XDECREF(s), Py_XDECREF(v), Py_XDECREF(o);
+  PyErr_Clear();
+  return out;
+}
+std::string list(at::IntArrayRef v) {
+  std::string s = "[";
+  for (size_t i = 0; i < v.size(); ++i) s += (i ? ", " : "") + std::to_string(v[i]);
+  return s + "]";
+}
+
+const at::Tensor& tensor(PyObject* o, Name what) {
+  if (!THPVariable_Check(o)) refuse_type(std::string(what) + " must be a tensor, got " + Py_TYPE(o)->tp_name);
+  return THPVariable_Unpack(o);
+}
+long long integer(PyObject* o, Name what) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised();
+  if (v < INT32_MIN || v > INT32_MAX) refuse_value(std::string(what) + " is out of range");
+  return v;
+}
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  return v;
+}
+void* address(PyObject* o) {
+  void* v = PyLong_AsVoidPtr(o);
+  if (!v && PyErr_Occurred()) throw Raised();
+  return v;
+}
+// None (the legacy default stream), a handle, or an object with one
+void* stream(PyObject* o) {
+  if (o == Py_None) return nullptr;
+  if (PyLong_Check(o)) return address(o);
+  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+  if (!h) throw Raised();
+  void* v = PyLong_AsVoidPtr(h);
+  Py_DECREF(h);
+  if (!v && PyErr_Occurred()) throw Raised();
+  return v;
+}
+int fits(int64_t v, Name what) {
+  if (v > INT32_MAX) refuse_value(std::string(what) + " is too large");
+  return (int)v;
+}
+
+// What the tensors of a call agree on
+struct Kind {
+  at::ScalarType type;
+  c10::Device device;
+};
+bool is(const at::Tensor& t, const Kind& k) { return t.scalar_type() == k.type && t.device() == k.device; }
+[[noreturn]] void wrong_kind(const at::Tensor& t, const Kind& k, Name what) {
+  refuse_type(std::string(what) + " must be a " + (k.type == at::kFloat ? "torch.float32" : "torch.bfloat16") +
+              " tensor on " + k.device.str() + ", got " + attribute(t, "dtype") + " on " + t.device().str());
+}
+Kind kind_of(const at::Tensor& t, Name what) {
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+    refuse_type("expected a bfloat16 or float32 tensor, got " + attribute(t, "dtype"));
+  if (!t.is_cuda()) refuse_type(std::string(what) + " must be a CUDA tensor");
+  return {t.scalar_type(), t.device()};
+}
+int code_of(const Kind& k) { return k.type == at::kFloat ? MOE_F32 : MOE_BF16; }
+
+// A tensor with contiguous rows and the shape of x
+const void* rows(PyObject* o, const Kind& k, at::IntArrayRef shape, Name what, long long& row) {
+  const at::Tensor& t = tensor(o, what);
+  if (!is(t, k)) wrong_kind(t, k, what);
+  if (t.sizes() != shape) refuse_value(std::string(what) + " must have shape " + list(shape) + ", got " + list(t.sizes()));
+  if (t.stride(1) != 1 && shape[1] > 1) refuse_value(std::string(what) + ": rows must be contiguous");
+  row = t.stride(0);
+  return t.data_ptr();
+}
+
+const void* vector(PyObject* o, const Kind& k, int64_t n, Name what) {
+  const at::Tensor& t = tensor(o, what);
+  if (!is(t, k)) wrong_kind(t, k, what);
+  if (t.dim() != 1 || t.size(0) != n || (n > 1 && t.stride(0) != 1))
+    refuse_value(std::string(what) + " must be a contiguous vector of " + std::to_string(n) + " entries");
+  return t.data_ptr();
+}
+
+// A contiguous int32 vector; of n entries if n >= 0
+const int32_t* ints(PyObject* o, c10::Device device, int64_t n, Name what) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.scalar_type() != at::kInt || t.device() != device || t.dim() != 1 || (n >= 0 && t.size(0) != n))
+    refuse_type(std::string(what) + " must be an int32 vector" + (n < 0 ? "" : " of " + std::to_string(n) + " entries") +
+                " on " + device.str());
+  if (t.stride(0) != 1 && t.size(0) > 1) refuse_value(std::string(what) + " must be contiguous");
+  return (const int32_t*)t.data_ptr();
+}
+int64_t entries(PyObject* o, Name what) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.dim() != 1) refuse_type(std::string(what) + " must be an int32 vector");
+  return t.size(0);
+}
+
+struct Heads {
+  void* p;
+  long long token, head;
+};
+Heads heads_of(const at::Tensor& t, const Kind& k, at::IntArrayRef shape, Name what) {
+  if (!is(t, k)) wrong_kind(t, k, what);
+  if (t.sizes() != shape) refuse_value(std::string(what) + " must have shape " + list(shape) + ", got " + list(t.sizes()));
+  if (t.stride(2) != 1 && shape[2] != 1) refuse_value(std::string(what) + ": the head dimension must be contiguous");
+  return {t.data_ptr(), t.stride(0), t.stride(1)};
+}
+
+float* lse_of(PyObject* o, c10::Device device, int64_t n, int64_t heads) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, "lse");
+  if (t.scalar_type() != at::kFloat || t.device() != device || t.dim() != 2 || t.size(0) != n || t.size(1) != heads ||
+      !t.is_contiguous())
+    refuse_type("lse must be a contiguous float32 tensor [" + std::to_string(n) + ", " + std::to_string(heads) + "] on " +
+                device.str());
+  return (float*)t.data_ptr();
+}
+
+// ------------------------------------------------------------------ entry points
+
+decltype(&moe_norm_residual) norm_entry;
+decltype(&moe_attn_prompt) prompt_entry;
+decltype(&moe_attn_decode) decode_entry;
+decltype(&moe_kv_append) append_entry;
+using ListEntry = moe_status (*)(const moe_kv_pages*, const int32_t*, const int32_t*, int, moe_stream_t);
+
+template <class F>
+PyObject* launch(F&& f) {
+  moe_status st;
+  Py_BEGIN_ALLOW_THREADS st = f();
+  Py_END_ALLOW_THREADS return PyLong_FromLong(st);
+}
+
+// Runs a call; its refusals become Python errors
+template <class F>
+PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
+  try {
+    if (got != want) refuse_type("wrong number of arguments");
+    return f();
+  } catch (const Refused& r) {
+    PyErr_SetString(r.type, r.why.c_str());
+  } catch (const Raised&) {
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  return guarded(count, 4, [&]() -> PyObject* {
+    norm_entry = (decltype(norm_entry))address(v[0]);
+    prompt_entry = (decltype(prompt_entry))address(v[1]);
+    decode_entry = (decltype(decode_entry))address(v[2]);
+    append_entry = (decltype(append_entry))address(v[3]);
+    Py_RETURN_NONE;
+  });
+}
+
+// x, block, pre_weight, x_out, y, post_weight, gate, res_scale, eps, stream
+PyObject* norm(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  return guarded(count, 10, [&] {
+    const at::Tensor& x = tensor(v[0], "x");
+    const Kind k = kind_of(x, "x");
+    if (x.dim() != 2) refuse_value("x must have shape [tokens, hidden]");
+    const at::IntArrayRef shape = x.sizes();
+    moe_norm_args a = {};
+    a.dtype = code_of(k), a.hidden = fits(shape[1], "hidden"), a.tokens = fits(shape[0], "tokens");
+    a.x_d = rows(v[0], k, shape, "x", a.x_row);
+    if (v[1] != Py_None) a.block_d = rows(v[1], k, shape, "block", a.block_row);
+    if (v[2] != Py_None) a.pre_w_d = vector(v[2], k, shape[1], "pre_weight");
+    if (v[3] != Py_None) a.x_out_d = const_cast<void*>(rows(v[3], k, shape, "x_out", a.x_out_row));
+    if (v[4] != Py_None) a.y_d = const_cast<void*>(rows(v[4], k, shape, "y", a.y_row));
+    if (v[5] != Py_None) a.post_w_d = vector(v[5], k, shape[1], "post_weight");
+    if (v[6] != Py_None) {
+      const at::Tensor& g = tensor(v[6], "gate");
+      if (!is(g, k)) wrong_kind(g, k, "gate");
+      const int64_t d = g.dim();
+      if (d < 1 || d > 2 || (d == 2 && g.size(0) != 1 && g.size(0) != shape[0]) ||
+          (g.size(d - 1) != 1 && g.size(d - 1) != shape[1]))
+        refuse_value("gate must broadcast to " + list(shape));
+      if (d == 2 && g.size(0) != 1) a.gate_row = g.stride(0);
+      if (g.size(d - 1) > 1) {
+        a.gate_col = 1;
+        if (g.stride(d - 1) != 1) refuse_value("gate rows must be contiguous");
+      }
+      a.gate_d = g.data_ptr();
+    }
+    a.res_scale = (float)number(v[7]), a.eps = (float)number(v[8]);
+    void* s = stream(v[9]);
+    return launch([&] { return norm_entry(&a, s); });
+  });
+}
+
+// q, k, v, starts_q, starts_k, out, scale, window, lse, stream
+PyObject* prompt(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  return guarded(count, 10, [&] {
+    const at::Tensor& q = tensor(v[0], "q");
+    const at::Tensor& keys = tensor(v[1], "k");
+    const Kind kind = kind_of(q, "q");
+    if (q.dim() != 3 || keys.dim() != 3) refuse_value("q, k and v must have shape [tokens, heads, head_dim]");
+    const int64_t dim = q.size(2), key_shape[3] = {keys.size(0), keys.size(1), dim};
+    const Heads qa = heads_of(q, kind, q.sizes(), "q"), ka = heads_of(keys, kind, key_shape, "k");
+    const Heads va = heads_of(tensor(v[2], "v"), kind, keys.sizes(), "v");
+    const Heads oa = heads_of(tensor(v[5], "out"), kind, q.sizes(), "out");
+    const at::Tensor& starts = tensor(v[3], "starts_q");
+    const int64_t n = starts.dim() ? starts.size(0) - 1 : -1;
+    if (n < 0) refuse_value("starts_q and starts_k need at least one entry");
+    moe_prompt_args a = {};
+    a.dtype = code_of(kind), a.heads = fits(q.size(1), "heads"), a.kv_heads = fits(keys.size(1), "kv_heads");
+    a.head_dim = fits(dim, "head_dim"), a.n = fits(n, "starts_q");
+    a.q_tokens = fits(q.size(0), "q_tokens"), a.k_tokens = fits(keys.size(0), "k_tokens");
+    a.starts_q_d = ints(v[3], kind.device, n + 1, "starts_q"), a.starts_k_d = ints(v[4], kind.device, n + 1, "starts_k");
+    a.q_d = qa.p, a.k_d = ka.p, a.v_d = va.p, a.out_d = oa.p;
+    a.lse_d = lse_of(v[8], kind.device, q.size(0), q.size(1));
+    a.q_token = qa.token, a.q_head = qa.head, a.k_token = ka.token, a.k_head = ka.head;
+    a.v_token = va.token, a.v_head = va.head, a.out_token = oa.token, a.out_head = oa.head;
+    a.scale = (float)(v[6] == Py_None ? std::pow((double)dim, -0.5) : number(v[6]));
+    a.window = (int)integer(v[7], "window");
+    void* s = stream(v[9]);
+    return launch([&] { return prompt_entry(&a, s); });
+  });
+}
+
+// Which tensors go with a cache: its K pool says
+struct Cache {
+  const moe_kv_pages* kv;
+  Kind kind;
+};
+Cache cache_of(PyObject* at, PyObject* pool) {
+  const at::Tensor& k = tensor(pool, "the cache's k");
+  return {(const moe_kv_pages*)address(at), {k.scalar_type(), k.device()}};
+}
+
+// cache, pool, layer, q, seqs, out, scale, window, lse, stream
+PyObject* attend(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  return guarded(count, 10, [&] {
+    const Cache c = cache_of(v[0], v[1]);
+    const at::Tensor& q = tensor(v[3], "q");
+    if (q.dim() != 3) refuse_value("q must have shape [n, heads, head_dim]");
+    const int64_t n = q.size(0), heads = q.size(1), shape[3] = {n, heads, c.kv->head_dim};
+    const Heads qa = heads_of(q, c.kind, shape, "q"), oa = heads_of(tensor(v[5], "out"), c.kind, shape, "out");
+    const int32_t* seqs = ints(v[4], c.kind.device, n, "seqs");
+    float* lse = lse_of(v[8], c.kind.device, n, heads);
+    const float scale = (float)(v[6] == Py_None ? std::pow((double)c.kv->head_dim, -0.5) : number(v[6]));
+    const int layer = (int)integer(v[2], "layer"), window = (int)integer(v[7], "window");
+    const int n32 = fits(n, "n"), heads32 = fits(heads, "heads");
+    void* s = stream(v[9]);
+    return launch([&] {
+      return decode_entry(c.kv, layer, qa.p, qa.token, qa.head, seqs, n32, heads32, scale, window, oa.p, oa.token, oa.head,
+                          lse, s);
+    });
+  });
+}
+
+// cache, pool, layer, seqs, starts, k, v, stream
+PyObject* append(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  return guarded(count, 8, [&] {
+    const Cache c = cache_of(v[0], v[1]);
+    const int64_t n = entries(v[3], "seqs");
+    const at::Tensor& k = tensor(v[5], "k");
+    const int64_t tokens = k.dim() ? k.size(0) : 0, shape[3] = {tokens, c.kv->kv_heads, c.kv->head_dim};
+    const Heads ka = heads_of(k, c.kind, shape, "k"), va = heads_of(tensor(v[6], "v"), c.kind, shape, "v");
+    const int32_t *seqs = ints(v[3], c.kind.device, n, "seqs"), *starts = ints(v[4], c.kind.device, n + 1, "starts");
+    const int layer = (int)integer(v[2], "layer"), n32 = fits(n, "n"), tokens32 = fits(tokens, "tokens");
+    void* s = stream(v[7]);
+    return launch([&] {
+      return append_entry(c.kv, layer, seqs, starts, n32, ka.p, ka.token, ka.head, va.p, va.token, va.head, tokens32, s);
+    });
+  });
+}
+
+// cache, pool, entry point, first list, second list (or None), their names, stream:
+// the calls that take two lists of the same length
+PyObject* lists(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  return guarded(count, 8, [&] {
+    const Cache c = cache_of(v[0], v[1]);
+    const auto entry = (ListEntry)address(v[2]);
+    Name first = PyUnicode_AsUTF8(v[5]), second = PyUnicode_AsUTF8(v[6]);
+    if (!first || !second) throw Raised();
+    const int64_t n = entries(v[3], first);
+    const int32_t* a = ints(v[3], c.kind.device, n, first);
+    const int32_t* b = v[4] == Py_None ? nullptr : ints(v[4], c.kind.device, n, second);
+    const int n32 = fits(n, first);
+    void* s = stream(v[7]);
+    return launch([&] { return entry(c.kv, a, b, n32, s); });
+  });
+}
+
+#define CALL(name) {#name, (PyCFunction)(void (*)())name, METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {CALL(bind), CALL(norm), CALL(prompt), CALL(attend), CALL(append), CALL(lists), {}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__torch_calls() { return PyModule_Create(&module); }

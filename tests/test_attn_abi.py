@@ -118,3 +118,15 @@ def test_tensors_in_host_memory_are_refused():
     pool, ints = torch.zeros(1, 4, 2, 16, 64), torch.zeros(4, dtype=torch.int32)
     with pytest.raises(TypeError, match="CUDA"):
         A.KVPages(pool, pool.clone(), ints.view(2, 2), ints[:2], ints)
+
+
+def test_wrong_objects_are_refused():
+    import torch
+    from expert_slot_cache_topk_gb300 import attention as A
+    x, starts = torch.zeros(2, 64, dtype=torch.float64), torch.tensor([0, 3], dtype=torch.int32)
+    with pytest.raises(TypeError, match="x must be a tensor, got list"):
+        A.norm_residual([1.0])
+    with pytest.raises(TypeError, match="got torch.float64"):
+        A.norm_residual(x, x)
+    with pytest.raises(TypeError, match="k must be a tensor, got NoneType"):
+        A.attn_prompt(x, None, None, starts, starts, x)
