@@ -33,6 +33,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Kernels of a few microseconds that follow one another: each lets the next one be
+// launched as soon as its own blocks are there, and before it reads or writes anything
+// waits for the end of the one ahead (which has waited for those ahead of it; a block
+// that has nothing to do waits too).  What a kernel ahead may write is read with plain
+// loads, not through the read-only path.
+__device__ __forceinline__ void follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// launches a kernel that calls follow()
+template <typename... P, typename... A>
+cudaError_t launch_following(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // N consecutive elements as f32; N * sizeof(T) is 16 or 32 (16-byte aligned), or N is 1
 template <typename T, int N>
 __device__ __forceinline__ void load_vec(const T* __restrict__ p, float (&v)[N]) {

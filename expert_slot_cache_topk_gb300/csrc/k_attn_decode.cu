@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
   const int items = a.kv_heads * w.chunks;           // per entry
   const int per = (a.n + kThreads - 1) / kThreads;   // entries of a thread
   const long long cap = (long long)a.max_pages << a.page_shift;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  follow();
 
   // the tokens of an entry; nothing for a row out of range
   auto fetch = [&](int i, int& row, int& len) {
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(1024) k_join(const Dec a, const Work w) {
   const int row = blockIdx.x % w.chunk, item = blockIdx.x / w.chunk;
   const int i = item / items, hc = item % items;
   const int kh = hc / w.chunks, g0 = hc % w.chunks * w.chunk;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  follow();
   if (blockIdx.x == 0 && threadIdx.x == 0) w.cut->ticket = 0;
   if (g0 + row >= a.group) return;
   const long long before = __ldcg(w.before + i), nb = __ldcg(w.before + i + 1) - before;
@@ -735,8 +735,7 @@ cudaError_t go(const Dec& a, const Work& w, cudaStream_t s) {
     }
   }
   const int sms = device_sm_count();
-  k_decode<Op><<<sms < kMaxGrid ? sms : kMaxGrid, Op::kWarps * 32, smem, s>>>(a, w);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_following(k_decode<Op>, sms < kMaxGrid ? sms : kMaxGrid, Op::kWarps * 32, smem, s, a, w);
   if (e != cudaSuccess) return e;
   // The join starts as k_decode's blocks end and waits for all of them.  Few rows
   // have many slots each: 32 warps; many rows have few: as many threads as columns.
@@ -744,15 +743,9 @@ cudaError_t go(const Dec& a, const Work& w, cudaStream_t s) {
   if (rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   const int cover = (a.D + 31) / 32 * 32;            // the last join needs a thread per column
   const int threads = rows <= 2 * sms ? 1024 : cover > 128 ? cover : 128;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows), cfg.blockDim = dim3(threads), cfg.stream = s;
-  cfg.attrs = attr, cfg.numAttrs = 1;
-  if (a.D <= 64) return cudaLaunchKernelEx(&cfg, k_join<typename Op::T, 2>, a, w);
-  if (a.D <= 128) return cudaLaunchKernelEx(&cfg, k_join<typename Op::T, 4>, a, w);
-  return cudaLaunchKernelEx(&cfg, k_join<typename Op::T, 8>, a, w);
+  if (a.D <= 64) return launch_following(k_join<typename Op::T, 2>, (unsigned)rows, threads, 0, s, a, w);
+  if (a.D <= 128) return launch_following(k_join<typename Op::T, 4>, (unsigned)rows, threads, 0, s, a, w);
+  return launch_following(k_join<typename Op::T, 8>, (unsigned)rows, threads, 0, s, a, w);
 }
 
 // query heads of an item: the group in equal parts of at most `most`

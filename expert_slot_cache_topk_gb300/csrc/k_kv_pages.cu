@@ -8,8 +8,7 @@
 // appended to: 19 us for the three calls).  Append, the private copies of shared pages
 // and compaction move K and V bytes once (read + write): 56 copied pages of 16 layers
 // 102 us with the calls around them (585 MB), 4099 pages compacted 337 us (2.1 GB, 6.3
-// TB/s).  A second kernel is launched while the first runs (programmatic dependent
-// launch) and waits for it before it reads what the first writes.
+// TB/s).  Each kernel is launched while the one ahead runs (follow()).
 #include "attn_common.cuh"
 
 namespace moe {
@@ -63,21 +62,6 @@ Kv make(const moe_kv_pages& m) {
   return d;
 }
 
-// Two kernels of one call: the second is launched while the first runs (its blocks
-// are there when the first one ends) and waits for all of it before it reads.
-__device__ __forceinline__ void first_of_two() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void second_of_two() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <typename... P, typename... A>
-cudaError_t launch_second(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
-  cfg.attrs = attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
 __device__ __forceinline__ void set_status(int32_t* status, int code) { atomicCAS(status, MOE_KV_OK, code); }
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
@@ -112,11 +96,11 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
 }
 
 // One block: n rows, in list order.
-__global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int32_t* __restrict__ seqs,
-                                                          const int32_t* __restrict__ counts, int n) {
+__global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int32_t* seqs, const int32_t* counts,
+                                                          int n) {
+  follow();
   __shared__ int bad, ncopy;
   const int t = threadIdx.x;
-  first_of_two();
   if (t == 0) bad = 0, ncopy = 0, d.hdr[H_COPIES] = 0;
   __syncthreads();
   for (int i = t; i < n; i += kBookThreads) {
@@ -235,7 +219,7 @@ __device__ __forceinline__ void copy_units(const char* __restrict__ src, char* _
 
 // Private copies of shared last pages: the tokens held, every layer, K and V
 __global__ void __launch_bounds__(256) k_copy_tails(const Kv d) {
-  second_of_two();
+  follow();
   const int copies = d.hdr[H_COPIES];
   const long long head_bytes = d.token_bytes << d.page_shift;
   const long long page_bytes = head_bytes * d.kv_heads;
@@ -253,7 +237,7 @@ __global__ void __launch_bounds__(256) k_copy_tails(const Kv d) {
 }
 
 // Whole pages from src[i] to dst[i], i < n, in every layer
-__device__ __forceinline__ void copy_pages(const Kv& d, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+__device__ __forceinline__ void copy_pages(const Kv& d, const int32_t* src, const int32_t* dst,
                                            int n) {
   const long long page_bytes = (d.token_bytes << d.page_shift) * d.kv_heads;
   const long long part = page_bytes < 65536 ? page_bytes : 65536;   // bytes of one item
@@ -275,14 +259,14 @@ __device__ __forceinline__ void copy_pages(const Kv& d, const int32_t* __restric
                       blockDim.x);
   }
 }
-__global__ void __launch_bounds__(256) k_copy_pages(const Kv d, const int32_t* __restrict__ src,
-                                                    const int32_t* __restrict__ dst, int n) {
+__global__ void __launch_bounds__(256) k_copy_pages(const Kv d, const int32_t* src, const int32_t* dst, int n) {
+  follow();
   copy_pages(d, src, dst, n);
 }
 
 // A list of rows is in range and has no row twice.  Each block decides for
 // itself from the same inputs, so that all of them go on or none does.
-__device__ __forceinline__ int check_rows(const int32_t* __restrict__ rows, int n, int max_seqs, unsigned* bits,
+__device__ __forceinline__ int check_rows(const int32_t* rows, int n, int max_seqs, unsigned* bits,
                                           bool distinct) {
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;
@@ -300,8 +284,8 @@ __device__ __forceinline__ int check_rows(const int32_t* __restrict__ rows, int 
   return r;
 }
 
-__global__ void __launch_bounds__(256) k_truncate(const Kv d, const int32_t* __restrict__ seqs,
-                                                  const int32_t* __restrict__ lens, int n) {
+__global__ void __launch_bounds__(256) k_truncate(const Kv d, const int32_t* seqs, const int32_t* lens, int n) {
+  follow();
   extern __shared__ unsigned bits[];
   __shared__ int neg;
   if (threadIdx.x == 0) neg = 0;
@@ -333,9 +317,8 @@ __global__ void __launch_bounds__(256) k_truncate(const Kv d, const int32_t* __r
 }
 
 // Fork, first launch: the sources' rows as they are, and one more reference each
-__global__ void __launch_bounds__(256) k_fork_read(const Kv d, const int32_t* __restrict__ src,
-                                                   const int32_t* __restrict__ dst, int n) {
-  first_of_two();
+__global__ void __launch_bounds__(256) k_fork_read(const Kv d, const int32_t* src, const int32_t* dst, int n) {
+  follow();
   extern __shared__ unsigned bits[];
   const int bad = check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true);
   if (bad) {
@@ -356,11 +339,10 @@ __global__ void __launch_bounds__(256) k_fork_read(const Kv d, const int32_t* __
 }
 
 // Fork, second launch: release what the destinations held, write their rows
-__global__ void __launch_bounds__(256) k_fork_write(const Kv d, const int32_t* __restrict__ src,
-                                                    const int32_t* __restrict__ dst, int n) {
+__global__ void __launch_bounds__(256) k_fork_write(const Kv d, const int32_t* src, const int32_t* dst, int n) {
+  follow();
   extern __shared__ unsigned bits[];
   const int bad = check_rows(src, n, d.max_seqs, bits, false) | check_rows(dst, n, d.max_seqs, bits, true);
-  second_of_two();                       // refused or not: this kernel's end is the call's end
   if (bad) return;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int s = dst[i], held = d.lens[s], now = d.mark[i];
@@ -384,11 +366,11 @@ __global__ void __launch_bounds__(256) k_fork_write(const Kv d, const int32_t* _
 // Append: one warp per (token, K or V), a lane per 16-byte (or narrower) unit of
 // the token's kv_heads rows
 template <typename U>
-__global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, const int32_t* __restrict__ seqs,
-                                                const int32_t* __restrict__ starts, int n,
-                                                const char* __restrict__ k, long long k_token, long long k_head,
-                                                const char* __restrict__ v, long long v_token, long long v_head,
-                                                int tokens) {
+__global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, const int32_t* seqs,
+                                                const int32_t* starts, int n, const char* k, long long k_token,
+                                                long long k_head, const char* v, long long v_token,
+                                                long long v_head, int tokens) {
+  follow();
   const int lane = threadIdx.x & 31;
   const int units = (int)(d.token_bytes / (long long)sizeof(U));
   const long long head_bytes = d.token_bytes << d.page_shift;
@@ -428,9 +410,9 @@ __global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, 
 // (list_b) in ascending order, the reference counts afterwards.  Eight pages to a
 // thread and round: a pool of 8192 pages is one round of each scan.
 __global__ void __launch_bounds__(kBookThreads) k_compact_plan(const Kv d, int32_t* refs_out, int32_t* used_out) {
+  follow();
   constexpr int kEach = 8, kRound = kEach * kBookThreads;
   const int t = threadIdx.x;
-  first_of_two();
   int used = 0;
   for (int p0 = 0; p0 < d.num_pages; p0 += kRound) {
     int mine = 0, total;
@@ -480,7 +462,7 @@ __global__ void __launch_bounds__(kBookThreads) k_compact_plan(const Kv d, int32
 // Compaction, second launch: every table entry that names a mover names its hole
 // (the movers are ascending, so an entry is found by bisection), and the pages move
 __global__ void __launch_bounds__(256) k_compact_move(const Kv d, int32_t* table_out) {
-  second_of_two();
+  follow();
   const int movers = d.hdr[H_MOVES];
   const long long n = (long long)d.max_seqs * d.max_pages;
   const int first = movers ? d.list_a[0] : 0x7fffffff;
@@ -515,12 +497,11 @@ cudaError_t launch_kv_reserve(const moe_kv_pages& kv, const int32_t* seqs, const
                               cudaStream_t s) {
   if (n <= 0) return cudaSuccess;
   const Kv d = make(kv);
-  k_reserve<<<1, kBookThreads, 0, s>>>(d, seqs, counts, n);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_following(k_reserve, 1, kBookThreads, 0, s, d, seqs, counts, n);
   if (e != cudaSuccess) return e;
   const long long most = (long long)n * kv.layers * 2 * kv.kv_heads;
   const int grid = device_sm_count() * 8;
-  return launch_second(k_copy_tails, most < grid ? (int)most : grid, 256, 0, s, d);
+  return launch_following(k_copy_tails, most < grid ? (int)most : grid, 256, 0, s, d);
 }
 
 cudaError_t launch_kv_append(const moe_kv_pages& kv, int layer, const int32_t* seqs, const int32_t* starts, int n,
@@ -534,44 +515,35 @@ cudaError_t launch_kv_append(const moe_kv_pages& kv, int layer, const int32_t* s
   const long long want = (2ll * tokens + 7) / 8;
   const int grid = (int)(want < most ? want : most);
   const bool wide = aligned(16, k, v, k_token * e, k_head * e, v_token * e, v_head * e);
-  if (wide)
-    k_append<uint4><<<grid, 256, 0, s>>>(d, off, seqs, starts, n, (const char*)k, k_token * e, k_head * e, (const char*)v,
-                                         v_token * e, v_head * e, tokens);
-  else
-    k_append<uint16_t><<<grid, 256, 0, s>>>(d, off, seqs, starts, n, (const char*)k, k_token * e, k_head * e,
-                                            (const char*)v, v_token * e, v_head * e, tokens);
-  return cudaGetLastError();
+  return launch_following(wide ? k_append<uint4> : k_append<uint16_t>, grid, 256, 0, s, d, off, seqs, starts, n,
+                          (const char*)k, k_token * e, k_head * e, (const char*)v, v_token * e, v_head * e, tokens);
 }
 
 cudaError_t launch_kv_truncate(const moe_kv_pages& kv, const int32_t* seqs, const int32_t* lens, int n,
                                cudaStream_t s) {
   if (n <= 0) return cudaSuccess;
-  k_truncate<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(make(kv), seqs, lens, n);
-  return cudaGetLastError();
+  return launch_following(k_truncate, rows_grid(n), 256, bitmap_bytes(kv), s, make(kv), seqs, lens, n);
 }
 
 cudaError_t launch_kv_fork(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
   if (n <= 0) return cudaSuccess;
   const Kv d = make(kv);
-  k_fork_read<<<rows_grid(n), 256, bitmap_bytes(kv), s>>>(d, src, dst, n);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_following(k_fork_read, rows_grid(n), 256, bitmap_bytes(kv), s, d, src, dst, n);
   if (e != cudaSuccess) return e;
-  return launch_second(k_fork_write, rows_grid(n), 256, bitmap_bytes(kv), s, d, src, dst, n);
+  return launch_following(k_fork_write, rows_grid(n), 256, bitmap_bytes(kv), s, d, src, dst, n);
 }
 
 cudaError_t launch_kv_copy(const moe_kv_pages& kv, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
   if (n <= 0) return cudaSuccess;
-  k_copy_pages<<<device_sm_count() * 8, 256, 0, s>>>(make(kv), src, dst, n);
-  return cudaGetLastError();
+  return launch_following(k_copy_pages, device_sm_count() * 8, 256, 0, s, make(kv), src, dst, n);
 }
 
 cudaError_t launch_kv_compact(const moe_kv_pages& kv, int32_t* table_out, int32_t* refs_out, int32_t* used,
                               cudaStream_t s) {
   const Kv d = make(kv);
-  k_compact_plan<<<1, kBookThreads, 0, s>>>(d, refs_out, used);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_following(k_compact_plan, 1, kBookThreads, 0, s, d, refs_out, used);
   if (e != cudaSuccess) return e;
-  return launch_second(k_compact_move, device_sm_count() * 8, 256, 0, s, d, table_out);
+  return launch_following(k_compact_move, device_sm_count() * 8, 256, 0, s, d, table_out);
 }
 
 }  // namespace moe
