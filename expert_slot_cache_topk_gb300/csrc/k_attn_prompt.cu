@@ -62,7 +62,7 @@ __device__ __forceinline__ bool not_finite(float v) { return !(fabsf(v) <= 3.402
 // Sequence i owns the tiles from starts[i] / rows + i on: enough of them for
 // its queries, and no two sequences share one.  Tiles past a sequence's last
 // query are empty: *r0 >= its length.
-__device__ __forceinline__ int tile_sequence(const int32_t* __restrict__ starts, int n, int b, int rows, int* r0) {
+__device__ __forceinline__ int tile_sequence(const int32_t* starts, int n, int b, int rows, int* r0) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -77,6 +77,7 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 
 template <typename T, int DP, int BM, int BN, bool VEC>
 __global__ void __launch_bounds__(256) k_prompt(const moe_prompt_args a) {
+  wait_ahead();
   constexpr int PIT = DP + 4;                  // row pitch: 16-byte aligned, rows 4 banks apart
   constexpr int RN = BM / 16, CN = BN / 16, DN = DP / 64;    // rows, keys and 4-column groups of a thread
   constexpr bool kAsync = VEC && sizeof(T) == 4;             // tiles are copied as they are, one ahead
@@ -312,8 +313,7 @@ cudaError_t go(const moe_prompt_args& a, cudaStream_t s) {
   }
   const long long grid = (long long)a.heads * (a.q_tokens / BM + a.n);
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  k_prompt<T, DP, BM, BN, VEC><<<(unsigned)grid, 256, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_following(k_prompt<T, DP, BM, BN, VEC>, (unsigned)grid, 256, smem, s, a);
 }
 
 // f32 with heads of up to DP elements, 16-byte aligned.  The four warps of a block share
@@ -327,6 +327,7 @@ cudaError_t go(const moe_prompt_args& a, cudaStream_t s) {
 // pipe 54% and the issue slots 50% busy; registers leave room for two warps to a scheduler.
 template <int DP, int RM>
 __global__ void __launch_bounds__(128, DP == 64 ? 2 : 1) k_prompt_keys(const moe_prompt_args a) {
+  wait_ahead();
   constexpr int W = 4, PIT = DP + 4, BM = 4 * RM, BK = 32, PP = 2 * BK + 4, NJ = DP / 32;
   constexpr int kWarp = 2 * BK * PIT + BM * PP;              // floats of a warp: K, V, P
   extern __shared__ float sm[];
@@ -541,8 +542,7 @@ cudaError_t go_keys(const moe_prompt_args& a, cudaStream_t s) {
   }
   const long long grid = (long long)a.heads * (a.q_tokens / (4 * RM) + a.n);
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  k_prompt_keys<DP, RM><<<(unsigned)grid, 128, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_following(k_prompt_keys<DP, RM>, (unsigned)grid, 128, smem, s, a);
 }
 
 template <typename T, bool VEC, int BM>

@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  wait_ahead();
   const uint32_t tmem = c.tmem;
   auto s_at = [&](int i) { return tmem + i * 128; };
   auto o_at = [&](int i) { return tmem + 256 + i * 128; };
@@ -934,8 +935,7 @@ cudaError_t go(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
   }
   const long long grid = (long long)(p.heads / p.pack) * p.slots;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  k_prompt_tc<DP><<<(unsigned)grid, kTcThreads, Shape<DP>::kSmem, s>>>(mq, mk, mv, p);
-  return cudaGetLastError();
+  return launch_following(k_prompt_tc<DP>, (unsigned)grid, kTcThreads, Shape<DP>::kSmem, s, mq, mk, mv, p);
 }
 
 }  // namespace

@@ -80,6 +80,7 @@ __device__ __forceinline__ float squares(const float (&v)[VEC], float root, floa
 // of the block, with a gate for every channel.
 template <typename T, int VEC, int NV, bool POST, bool GATE>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 256) k_norm_row(const NormArgs a) {
+  follow();
   __shared__ __align__(16) float red[2][32];
   const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5, H = a.hidden;
   const float root = rsqrtf((float)H);
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 256) k_norm_row(const NormArg
 // G lanes per row, one access each; the next row is on its way meanwhile
 template <typename T, int VEC, int G, bool POST, bool GATE>
 __global__ void __launch_bounds__(256) k_norm_part(const NormArgs a) {
+  follow();
   const int t = threadIdx.x % G, c = t * VEC, H = a.hidden;
   const long long step = (long long)gridDim.x * blockDim.x / G;
   const bool on = c < H;
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(256) k_norm_part(const NormArgs a) {
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a) {
+  follow();
   __shared__ __align__(16) float red[2][32];
   extern __shared__ float keep[];              // x' of the row
   const int H = a.hidden, warps = blockDim.x >> 5, step = blockDim.x * VEC;
@@ -319,8 +322,7 @@ cudaError_t launch(const NormArgs& a, int threads, size_t smem, int rows, cudaSt
     const long long resident = (long long)device_sm_count() * (long long)(got & 255);
     grid = want < resident ? want : resident;
   }
-  kKernel<<<(unsigned)grid, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_following(kKernel, (unsigned)grid, threads, smem, s, a);
 }
 
 template <typename T, int VEC, int NV>
