@@ -68,8 +68,12 @@ struct Work {
   int chunk, chunks;             // query heads per item, items per key head
 };
 __host__ __device__ constexpr int slot_size(int chunk, int D) { return (chunk * (D + 2) + 3) / 4 * 4; }
+// a / b of numbers that are not negative; with 32 bits, several times faster, where they do
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 __device__ __forceinline__ int run_of(const Cut& c, long long u) {
-  const int b = (int)(u / c.stretch), off = (int)(u - b * c.stretch), own = c.warps * c.pw;
+  const int b = (int)quotient(u, c.stretch), off = (int)(u - b * c.stretch), own = c.warps * c.pw;
   return b * c.runs + (off < own ? off / c.pw : c.warps + (off - own) / c.pc);
 }
 __device__ __forceinline__ long long run_start(const Cut& c, int run) {
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
   Cut cut;
   cut.all = total * items;
   cut.warps = kWarps;
-  const long long each = (cut.all + gridDim.x - 1) / gridDim.x;        // of a thread block
+  const long long each = quotient(cut.all + gridDim.x - 1, gridDim.x);  // of a thread block
   cut.pc = (int)(each * kShareNum / kShareDen / kWarps);
   if (cut.pc >= Op::kStages) {                       // (so the loads are never two runs ahead of the products)
     cut.runs = 2 * kWarps;
@@ -524,9 +528,9 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
       u -= nb;
     }
     const int nb = blocks_of(c.from, c.len);
-    c.hc = (int)(u / nb);
+    c.hc = (int)quotient(u, nb);
     c.end = c.from / kBlock + nb;
-    c.blk = c.from / kBlock + (int)(u % nb);
+    c.blk = c.from / kBlock + (int)(u - (long long)c.hc * nb);
     return true;
   };
   // page of token (lane % kBlock) of the cursor's block
@@ -643,7 +647,8 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) k_join(const Dec a, const Work w) {
   __shared__ float sh[32][32 * VEC + 2];
-  const int items = a.kv_heads * w.chunks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int items = a.kv_heads * w.chunks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int warps = blockDim.x >> 5;
   const int row = blockIdx.x % w.chunk, item = blockIdx.x / w.chunk;
   const int i = item / items, hc = item % items;
   const int kh = hc / w.chunks, g0 = hc % w.chunks * w.chunk;
@@ -703,6 +708,7 @@ __global__ void __launch_bounds__(1024) k_join(const Dec a, const Work w) {
   if (lane == 0) sh[warp][32 * VEC] = m, sh[warp][32 * VEC + 1] = l;
   __syncthreads();
   if (warp * 32 >= a.D) return;
+  warps = rb - ra + 1 < warps ? rb - ra + 1 : warps;          // those that had slots
   m = lane < warps ? sh[lane][32 * VEC] : -INFINITY;
   m = warp_max(m);
   const float scale = lane < warps ? (sh[lane][32 * VEC] == -INFINITY ? 1.f : exp2f(sh[lane][32 * VEC] - m)) : 0.f;

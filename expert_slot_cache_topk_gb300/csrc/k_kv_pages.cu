@@ -99,8 +99,11 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
 __global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int32_t* seqs, const int32_t* counts,
                                                           int n) {
   follow();
-  __shared__ int bad, ncopy;
+  __shared__ int bad, ncopy, off_near[kBookThreads + 1], copy_near[kBookThreads];
   const int t = threadIdx.x;
+  // where each row's run of pages starts; 1 if the run starts with a private copy
+  int* off = n <= kBookThreads ? off_near : d.off;
+  int* copies = n <= kBookThreads ? copy_near : d.mark;
   if (t == 0) bad = 0, ncopy = 0, d.hdr[H_COPIES] = 0;
   __syncthreads();
   for (int i = t; i < n; i += kBookThreads) {
@@ -135,11 +138,11 @@ __global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int3
     }
     int total;
     const int at = block_scan(want, &total);
-    if (i < n) d.off[i] = base + at;
+    if (i < n) off[i] = base + at;
     base += total;
     if (base > d.num_pages) break;       // more than there are pages: refused below
   }
-  if (t == 0) d.off[n] = base;
+  if (t == 0) off[n] = base;
   __syncthreads();
   if (bad || base > d.num_pages) {
     if (t == 0) set_status(d.status, bad ? bad : MOE_KV_NO_PAGES);
@@ -173,22 +176,22 @@ __global__ void __launch_bounds__(kBookThreads) k_reserve(const Kv d, const int3
   // hand them out: page r of the list goes to the row whose run holds r.  Shared
   // pages are judged by the counts as they were: the reads come before any change.
   for (int i = t; i < n; i += kBookThreads) {
-    const int s = seqs[i], held = d.lens[s], after = held + counts[i];
+    const int held = d.lens[seqs[i]], after = held + counts[i];
     const int fresh = pages_of(after, d.page_shift) - pages_of(held, d.page_shift);
-    d.mark[s] = d.off[i + 1] - d.off[i] > fresh;         // 1: the run starts with a private copy
+    copies[i] = off[i + 1] - off[i] > fresh;
   }
   __syncthreads();
   for (int r = t; r < base; r += kBookThreads) {
     int lo = 0, hi = n;                                   // off[lo] <= r < off[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (d.off[mid] <= r) lo = mid;
+      if (off[mid] <= r) lo = mid;
       else hi = mid;
     }
     const int s = seqs[lo], held = d.lens[s], page = d.list_a[r];
-    const int col = pages_of(held, d.page_shift) + (r - d.off[lo]) - d.mark[s];
+    const int col = pages_of(held, d.page_shift) + (r - off[lo]) - copies[lo];
     int32_t* cell = d.table + (size_t)s * d.max_pages + col;
-    if (d.mark[s] && r == d.off[lo]) {
+    if (copies[lo] && r == off[lo]) {
       const int c = atomicAdd(&ncopy, 1);                 // the order of copies does not matter
       const int old = *cell;
       d.cp[3 * c] = old, d.cp[3 * c + 1] = page, d.cp[3 * c + 2] = held & ((1 << d.page_shift) - 1);
@@ -377,14 +380,15 @@ __global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, 
   const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
   for (long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < 2ll * tokens; w += warps) {
     const int t = (int)(w >> 1), side = (int)(w & 1);
-    int lo = 0, hi = n;                       // starts[lo] <= t < starts[hi]
+    int lo = 0, hi = n;                       // starts[lo] <= t < starts[hi]; the lanes look at 32 places at once
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (starts[mid] <= t) lo = mid;
-      else hi = mid;
+      const int step = (hi - lo + 31) / 32, x = lo + lane * step;
+      const unsigned below = __ballot_sync(kAll, lane == 0 || (x < hi && starts[x] <= t));
+      lo += (31 - __clz(below)) * step;
+      hi = lo + step < hi ? lo + step : hi;
     }
-    const int s = seqs[lo], end = starts[lo + 1];
-    if (t < starts[lo] || t >= end || (unsigned)s >= (unsigned)d.max_seqs) {
+    const int s = seqs[lo], first = starts[lo], end = starts[lo + 1];
+    if (t < first || t >= end || (unsigned)s >= (unsigned)d.max_seqs) {
       if (lane == 0) set_status(d.status, MOE_KV_BAD_SEQ);
       continue;
     }
@@ -399,9 +403,20 @@ __global__ void __launch_bounds__(256) k_append(const Kv d, long long pool_off, 
                (pos & ((1 << d.page_shift) - 1)) * d.token_bytes;
     const char* from = side ? v + t * v_token : k + t * k_token;
     const long long from_head = side ? v_head : k_head;
-    for (int u = lane; u < units * d.kv_heads; u += 32) {
-      const int h = u / units, x = u - h * units;
-      reinterpret_cast<U*>(to + h * head_bytes)[x] = reinterpret_cast<const U*>(from + h * from_head)[x];
+    const int all = units * d.kv_heads;
+    constexpr int kAhead = 4;                 // loads under way at once
+    for (int u0 = lane; u0 < all; u0 += 32 * kAhead) {
+      U got[kAhead];
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z) {
+        const int u = u0 + 32 * z, h = u / units;
+        if (u < all) got[z] = reinterpret_cast<const U*>(from + h * from_head)[u - h * units];
+      }
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z) {
+        const int u = u0 + 32 * z, h = u / units;
+        if (u < all) reinterpret_cast<U*>(to + h * head_bytes)[u - h * units] = got[z];
+      }
     }
   }
 }
