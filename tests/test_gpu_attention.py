@@ -226,6 +226,30 @@ def test_reserve_copies_only_the_tokens_held_and_shares_nothing(A):
         assert torch.equal(bits(kv.k[:, new, :, held:]), bits(before_k[:, new, :, held:]))
 
 
+def test_reserve_and_append_for_thousands_of_sequences(A):
+    """More rows than the bookkeeping block has threads; half of them share their last page with a fork."""
+    rng = np.random.default_rng(5)
+    kv, host = new_cache(A, layers=1, page=16, pages=9000, seqs=3000, cols=4)
+    first, counts = rng.permutation(1500), rng.integers(0, 21, 1500)
+    kv.reserve(ints(first), ints(counts))
+    host.reserve(first, counts)
+    kv.fork(ints(range(1500)), ints(range(1500, 3000)))
+    host.fork(range(1500), range(1500, 3000))
+    seqs, more = rng.permutation(3000)[:2600], rng.integers(0, 4, 2600)
+    kv.reserve(ints(seqs), ints(more))
+    host.reserve(seqs, more)
+    kv.check()
+    assert_state(kv, host)
+    starts = np.concatenate([[0], np.cumsum(more)])
+    new = randn(gen(1), int(starts[-1]), kv.kv_heads, kv.head_dim, dtype=kv.k.dtype)
+    kv.append(0, ints(seqs), ints(starts), new, -new)
+    kv.check()
+    lens, table = kv.lens.cpu().numpy(), kv.table.cpu().numpy()
+    at = [(table[s, t // 16], t % 16) for s, n in zip(seqs, more) for t in range(lens[s] - n, lens[s])]
+    page, off = (torch.tensor(x, device="cuda") for x in zip(*at))
+    assert torch.equal(bits(kv.k[0, page, :, off]), bits(new)) and torch.equal(bits(kv.v[0, page, :, off]), bits(-new))
+
+
 def test_compact_out_of_place_keeps_the_old_table(A):
     rng = np.random.default_rng(0)
     kv, host = new_cache(A, pages=80, seqs=8, cols=12)
