@@ -26,6 +26,7 @@ struct Dec {
   long long q_token, q_head, out_token, out_head;
   int n, heads, group, window;
   float scale;
+  int pairs;                         // two elements of q, or of out, are read and written at once
 };
 
 // How the work is laid out.  An item is (list entry, key head, chunk of its query
@@ -81,6 +82,15 @@ __device__ __forceinline__ long long run_start(const Cut& c, int run) {
   return b * c.stretch + (k < c.warps ? k * c.pw : c.warps * c.pw + (k - c.warps) * c.pc);
 }
 
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y, bool pairs) {
+  if (pairs) *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y);
+  else Elem<__nv_bfloat16>::put(p, x), Elem<__nv_bfloat16>::put(p + 1, y);
+}
+__device__ __forceinline__ void put2(float* p, float x, float y, bool pairs) {
+  if (pairs) *reinterpret_cast<float2*>(p) = make_float2(x, y);
+  else p[0] = x, p[1] = y;
+}
+
 // The item at hand and a block of it
 struct Cursor {
   int i, hc;                     // list entry; key head * chunks + chunk
@@ -124,17 +134,24 @@ struct Bf16 {
     const int kh = c.hc / w.chunks, g0 = c.hc % w.chunks * w.chunk;
     const int r = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int x = 0; x < DP / 16; ++x)
+    for (int h = 0; h < 2; ++h) {
+      const int g = r + 8 * h;
+      const bool on = !(SMALL && h) && g < w.chunk && g0 + g < a.group;
+      const T* p = (const T*)a.q + c.i * a.q_token + (kh * a.group + g0 + (on ? g : 0)) * a.q_head + 2 * t;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int g = r + (y & 1) * 8, d = 16 * x + (y >> 1) * 8 + 2 * t;
+      for (int x = 0; x < DP / 8; ++x) {
         uint32_t v = 0;
-        if (g < w.chunk && g0 + g < a.group && d < a.D) {
-          const T* p = (const T*)a.q + c.i * a.q_token + (kh * a.group + g0 + g) * a.q_head + d;
-          v = (uint32_t) * reinterpret_cast<const unsigned short*>(p) | (uint32_t) * reinterpret_cast<const unsigned short*>(p + 1) << 16;
+        if (on && 8 * x < a.D) {
+          if (a.pairs) {
+            v = *reinterpret_cast<const uint32_t*>(p + 8 * x);
+          } else {
+            const unsigned short* one = reinterpret_cast<const unsigned short*>(p + 8 * x);
+            v = (uint32_t)one[0] | (uint32_t)one[1] << 16;
+          }
         }
-        q[x][y] = v;
+        q[x / 2][2 * (x & 1) + h] = v;
       }
+    }
 #pragma unroll
     for (int x = 0; x < DP / 8; ++x)
 #pragma unroll
@@ -613,8 +630,8 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
       op.each(rows, a.D, lane,
               [&](int q, int d, float x, float y, float l) {
                 const float f = l == 0.f ? 0.f : 1.f / l;
-                Elem<T>::put(to + q * a.out_head + d, l == 0.f ? 0.f : x * f);
-                Elem<T>::put(to + q * a.out_head + d + 1, l == 0.f ? 0.f : y * f);
+                if (l == 0.f) x = y = 0.f;
+                put2(to + q * a.out_head + d, x * f, y * f, a.pairs);
               },
               [&](int q, float m, float l) {
                 if (lse) lse[q] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
@@ -783,6 +800,9 @@ cudaError_t launch_attn_decode(const moe_kv_pages& kv, const DecodeArgs& m, cuda
   a.kv_heads = kv.kv_heads, a.D = kv.head_dim;
   a.q = m.q, a.out = m.out, a.lse = m.lse;
   a.q_token = m.q_token, a.q_head = m.q_head, a.out_token = m.out_token, a.out_head = m.out_head;
+  const int two = 2 * (int)e;
+  a.pairs = aligned(two, a.q, a.out, a.q_token * (long long)e, a.q_head * (long long)e, a.out_token * (long long)e,
+                    a.out_head * (long long)e);
   a.n = m.n, a.heads = m.heads, a.group = m.heads / kv.kv_heads, a.window = m.window, a.scale = m.scale;
   Work w;
   char* work = (char*)kv.work_d + kv_work_bytes(kv);
