@@ -91,6 +91,14 @@ __device__ __forceinline__ void put2(float* p, float x, float y, bool pairs) {
   else p[0] = x, p[1] = y;
 }
 
+__device__ __forceinline__ float2 get2(const float* p, bool pairs) {
+  return pairs ? *reinterpret_cast<const float2*>(p) : make_float2(p[0], p[1]);
+}
+__device__ __forceinline__ float2 get2(const __nv_bfloat16* p, bool pairs) {
+  if (!pairs) return make_float2(__bfloat162float(p[0]), __bfloat162float(p[1]));
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+
 // The item at hand and a block of it
 struct Cursor {
   int i, hc;                     // list entry; key head * chunks + chunk
@@ -306,54 +314,73 @@ struct Plain {
 #pragma unroll
       for (int x = 0; x < NC; ++x)
 #pragma unroll
-        for (int y = 0; y < W; ++y) {
+        for (int y = 0; y < W; y += 2) {
           const int d = (e + 8 * x) * W + y;
-          q[g][x][y] = on && d < a.D ? Elem<T>::get(p + d) : 0.f;
-          o[g][x][y] = 0.f;
+          float2 two = make_float2(0.f, 0.f);
+          if (on && d < a.D) two = get2(p + d, a.pairs);
+          q[g][x][y] = two.x, q[g][x][y + 1] = two.y;
+          o[g][x][y] = o[g][x][y + 1] = 0.f;
         }
     }
   }
   __device__ __forceinline__ void block(uint32_t kt, unsigned live, float scale, int lane) {
-    const int e = lane & 7;
-#pragma unroll 1
-    for (int t = lane >> 3; t < kBlock; t += 4) {
-      float v[NC][W], s[GC];
+    const int e = lane & 7, t0 = lane >> 3;
+    constexpr int kPer = kBlock / 4;                   // tokens of a lane group: all scores first, then one rescale
+    float s[kPer][GC], v[NC][W];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int t = t0 + 4 * u;
 #pragma unroll
       for (int x = 0; x < NC; ++x) load(kt + t * kRow + (((e + 8 * x) ^ (t & 7)) << 4), v[x]);
 #pragma unroll
       for (int g = 0; g < GC; ++g) {
-        s[g] = 0.f;
+        s[u][g] = 0.f;
 #pragma unroll
         for (int x = 0; x < NC; ++x)
 #pragma unroll
-          for (int y = 0; y < W; ++y) s[g] = fmaf(q[g][x][y], v[x][y], s[g]);
+          for (int y = 0; y < W; ++y) s[u][g] = fmaf(q[g][x][y], v[x][y], s[u][g]);
       }
+    }
 #pragma unroll
-      for (int z = 1; z < 8; z <<= 1)
+    for (int z = 1; z < 8; z <<= 1)
 #pragma unroll
-        for (int g = 0; g < GC; ++g) s[g] += __shfl_xor_sync(kAll, s[g], z);
+      for (int u = 0; u < kPer; ++u)
+#pragma unroll
+        for (int g = 0; g < GC; ++g) s[u][g] += __shfl_xor_sync(kAll, s[u][g], z);
+#pragma unroll
+    for (int g = 0; g < GC; ++g) {
+      float mn = m[g];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        s[u][g] = live >> (t0 + 4 * u) & 1u ? s[u][g] * scale : -INFINITY;
+        mn = fmaxf(mn, s[u][g]);
+      }
+      if (mn > m[g]) {
+        const float f = exp2f(m[g] - mn);
+        m[g] = mn, l[g] *= f;
+#pragma unroll
+        for (int x = 0; x < NC; ++x)
+#pragma unroll
+          for (int y = 0; y < W; ++y) o[g][x][y] *= f;
+      }
+      const float mb = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        s[u][g] = exp2f(s[u][g] - mb);
+        l[g] += s[u][g];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int t = t0 + 4 * u;
 #pragma unroll
       for (int x = 0; x < NC; ++x) load(kt + (kBlock + t) * kRow + (((e + 8 * x) ^ (t & 7)) << 4), v[x]);
-      if (live >> t & 1u) {
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
-          s[g] *= scale;
-          if (s[g] > m[g] || m[g] == -INFINITY) {
-            const float mn = fmaxf(m[g], s[g]), f = mn == -INFINITY ? 1.f : exp2f(m[g] - mn);
-            m[g] = mn, l[g] *= f;
+      for (int g = 0; g < GC; ++g)
 #pragma unroll
-            for (int x = 0; x < NC; ++x)
+        for (int x = 0; x < NC; ++x)
 #pragma unroll
-              for (int y = 0; y < W; ++y) o[g][x][y] *= f;
-          }
-          const float p = exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g]));
-          l[g] += p;
-#pragma unroll
-          for (int x = 0; x < NC; ++x)
-#pragma unroll
-            for (int y = 0; y < W; ++y) o[g][x][y] = fmaf(p, v[x][y], o[g][x][y]);
-        }
-      }
+          for (int y = 0; y < W; ++y) o[g][x][y] = fmaf(s[u][g], v[x][y], o[g][x][y]);
     }
   }
   static __device__ __forceinline__ void load(uint32_t at, float (&v)[W]) {
