@@ -35,8 +35,8 @@ struct Dec {
 // thread block gets an equal stretch, whatever items lie in it: the host need not
 // know the lengths.  A stretch is cut into runs: one for each warp, and at its end
 // as many shorter ones (kShare of it) that any warp of the grid takes by ticket
-// when it is done, because SMs differ in how fast they get memory (without tickets
-// the median SM was done at 93 us, the last at 111).
+// when it is done, because SMs differ in how fast they get memory (without tickets the
+// median SM was done at 93 us when the last was at 111).
 //
 // A run that has a whole item writes its output; otherwise it leaves its maxima,
 // sums and unnormalised outputs in its two slots of the workspace (one for the item
@@ -48,8 +48,9 @@ struct Dec {
 // asynchronous copies ahead of use (page numbers one block further ahead), so no
 // barrier runs inside the loop.  What bounds it is memory: each key and value is
 // read once per chunk of query heads (64 sequences of up to 8192 tokens, 4 key heads
-// of 128, bf16, 530 MB: 93 us, 6.2 TB/s between the first block's arrival and the last
-// one; 106 us with k_join and the launches.  One of 131072, 268 MB: 58 us).
+// of 128, bf16, 530 MB: 87 us, 6.7 TB/s between the first block's arrival and the last
+// one; 94 us a call with k_join.  One of 131072, 268 MB: 55 us; one of 333, 16 heads: 13
+// us, two chains of dependent loads).
 constexpr int kMaxWarps = 12;                    // of a block of threads
 constexpr int kMaxGrid = 160;                    // blocks of threads, at most (one per SM)
 constexpr int kMaxChunk = 16;                    // query heads of an item

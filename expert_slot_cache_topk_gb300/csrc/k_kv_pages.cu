@@ -5,9 +5,9 @@
 //
 // What bounds these calls: the bookkeeping is a few kilobytes and costs
 // launches and dependent loads (64 sequences truncated, given room for 3 tokens and
-// appended to: 19 us for the three calls).  Append, the private copies of shared pages
+// appended to: 13 us for the three calls).  Append, the private copies of shared pages
 // and compaction move K and V bytes once (read + write): 56 copied pages of 16 layers
-// 102 us with the calls around them (585 MB), 4099 pages compacted 337 us (2.1 GB, 6.3
+// 98 us with the calls around them (585 MB), 4099 pages compacted 331 us (2.1 GB, 6.3
 // TB/s).  Each kernel is launched while the one ahead runs (follow()).
 #include "attn_common.cuh"
 

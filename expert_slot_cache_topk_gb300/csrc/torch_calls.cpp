@@ -1,7 +1,7 @@
 // The calls of attention.py: arguments checked on torch tensors and handed to the C
 // entry points of moe_attn.h.  Written against torch's C++ tensors because a call of
 // few tokens is bound by the caller: with the same checks in Python a norm took 14.5
-// us, outputs' allocation and launch included, of which the kernel is 3.
+// us, outputs' allocation and launch included, of which the kernel is 2; it takes 8.
 //
 // A function returns the entry point's status; a wrong argument raises TypeError or
 // ValueError before any of the library is called.  The entry points' addresses come
