@@ -49,7 +49,7 @@ struct Dec {
 // barrier runs inside the loop.  What bounds it is memory: each key and value is
 // read once per chunk of query heads (64 sequences of up to 8192 tokens, 4 key heads
 // of 128, bf16, 530 MB: 87 us, 6.7 TB/s between the first block's arrival and the last
-// one; 94 us a call with k_join.  One of 131072, 268 MB: 55 us; one of 333, 16 heads: 13
+// one; 94 us a call with k_join.  One of 131072, 268 MB: 55 us; one of 333, 16 heads: 10
 // us, two chains of dependent loads).
 constexpr int kMaxWarps = 12;                    // of a block of threads
 constexpr int kMaxGrid = 160;                    // blocks of threads, at most (one per SM)
@@ -497,8 +497,9 @@ __global__ void __launch_bounds__(Op::kWarps * 32, 1) k_decode(const Dec a, cons
   } else {
     cut.runs = kWarps;
     cut.pc = 1;
-    cut.pw = (int)((each + kWarps - 1) / kWarps);
-    if (cut.pw < 2) cut.pw = 2;
+    // (few blocks: one for each warp, on as few SMs as that takes, because each SM fetches
+    // the code anew: 333 tokens, 16 heads: 10.3 us; spread over the SMs 13, two a warp 12.2)
+    cut.pw = each > 0 ? (int)((each + kWarps - 1) / kWarps) : 1;
     cut.stretch = kWarps * cut.pw;
   }
   if (blockIdx.x == 0) {                             // for k_join
