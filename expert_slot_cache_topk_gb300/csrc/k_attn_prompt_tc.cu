@@ -30,7 +30,8 @@
 // longer than the other tile's products that run under it (3,100 cycles for both
 // tiles and 128 keys, 2,048 of them products), and shared memory, whose full rate the
 // score products need while TMA writes the next tiles.  16384 tokens, 16 heads of 128:
-// 727 us, 1.5 PFLOP/s; 24 prompts of up to 1500 tokens, 20 heads: 122 us.
+// 727 us, 1.5 PFLOP/s, again and again on the same inputs (786 in turn with other
+// inputs); 24 prompts of up to 1500 tokens, 20 heads: 122 us.
 //
 // The running maximum is lazy: m grows only when a row's maximum exceeds it by
 // more than 8 (weights then stay below 2^8, exact in the same relative
